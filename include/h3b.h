@@ -417,6 +417,122 @@ H3B_API h3b_status h3b_gemm_i8_gelu(const int8_t* A, const float* sA, const int8
                             const float* bias, void* g, float* absmax, int M, int N, int K,
                             h3b_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Attention over selected key blocks, per-head normalised Q/K with positions
+ * per token, and branch norms around the gated residual. Steps of their own
+ * beside h3b_qkv_projection, h3b_attention and the gated residual GEMMs, with
+ * the same conventions (device pointers, 16-byte alignment, host checks before
+ * any launch, asynchronous on `stream`, no allocation).
+ * ------------------------------------------------------------------------- */
+
+/* Per-head RMSNorm of Q and K and rotary positions on three axes given per
+ * token, from a token-major projection to the head-major layout.
+ *   qkv  bf16 [B*L][row_stride]: columns n_heads*head_dim of Q, then
+ *        n_kv_heads*head_dim of K, then as many of V; the columns after them
+ *        (row_stride is a multiple of 8 and at least
+ *        (n_heads + 2 n_kv_heads) * head_dim) are not read.
+ *   q    bf16 [B][n_heads][L][head_dim]; k, v bf16 [B][n_kv_heads][L][head_dim].
+ *        No output may overlap qkv or another output.
+ *   wq, wk: fp32 [head_dim] norm weights; NULL leaves that part unnormalised.
+ *        With weights, y = x * rsqrt(mean(x^2) + norm_eps) * w over the head.
+ *   pos  fp32 [B][L][3]: the token's (t, h, w) position, fractions allowed;
+ *        NULL rotates nothing. Lanes [0, rope_t) rotate with t, the next rope_h
+ *        with h, the next rope_w with w, each part even, their sum at most
+ *        head_dim; the lanes after them pass unrotated. Pair (2j, 2j+1) of a
+ *        part of length r turns by pos * rope_theta^(-2j/r); the angle is formed
+ *        and reduced in 64 bits, so positions far from zero lose nothing.
+ *   Norm and rotation are in fp32, each output rounded once; V is copied.
+ *   n_heads >= 1, n_kv_heads >= 1, n_heads + n_kv_heads <= 1024, head_dim in
+ *   {64, 128}, B*L < 2^31; B*L == 0 is an empty problem. */
+typedef struct {
+  int B, L;
+  int n_heads, n_kv_heads, head_dim;
+  int rope_t, rope_h, rope_w;
+  float rope_theta, norm_eps;
+  long long row_stride;
+} h3b_qk_dims;
+H3B_API h3b_status h3b_qk_norm_rope(const h3b_qk_dims* dims, const void* qkv, const float* wq, const float* wk,
+                                    const float* pos, void* q, void* k, void* v, h3b_stream stream);
+
+/* Block-sparse attention. Queries are taken in blocks of 128 consecutive
+ * tokens, nqb = ceil(Lq / 128) of them per head; keys in blocks of block_k (64
+ * or 128), nkb = ceil(Lk / block_k). Every query block of every head has a list
+ * of up to topk key blocks.
+ *   q bf16 [B][n_heads][Lq][head_dim]; k, v bf16 [B][n_kv_heads][Lk][head_dim]:
+ *   query head h reads key head h / (n_heads / n_kv_heads).
+ *   q_lens, kv_lens: int32 [B], the valid tokens of each item (device), values
+ *   are clamped to [0, Lq] and [0, Lk]; NULL: all. Rows of q, k and v behind
+ *   them are never used, whatever they hold.
+ *   blocks int32 [B][n_heads][nqb][topk], counts int32 [B][n_heads][nqb].
+ *   Limits: head_dim in {64, 128}; n_heads a multiple of n_kv_heads;
+ *   B * n_heads <= 65535; B*Lq and B*Lk < 2^31; Lk >= 1; nkb <= 4096;
+ *   1 <= topk <= nkb; keep_first, keep_local >= 0, with keep_first plus the
+ *   blocks that keep_local can add at most topk. Lq == 0 or B == 0 is an empty
+ *   problem. */
+typedef struct {
+  int B, n_heads, n_kv_heads, head_dim;
+  int Lq, Lk;
+  int block_k, topk;
+  int keep_first, keep_local;
+} h3b_sparse_dims;
+
+/* Bytes of scratch that h3b_select_blocks and h3b_attention_blocks need (the
+ * larger of the two; 256-byte aligned). Two calls that may run at the same time
+ * need a workspace each. */
+H3B_API h3b_status h3b_sparse_workspace_size(const h3b_sparse_dims* dims, size_t* bytes);
+
+/* The key blocks each query block attends. The score of a pair is the product of
+ * the mean of the query block's valid rows and the mean of the key block's valid
+ * rows, summed in 64 bits. Of the key blocks that hold a valid key, the topk (or
+ * all, if fewer) with the highest scores are listed in ascending order in
+ * `blocks`, and their number is written to `counts`; unused entries are -1. Ties
+ * go to the lower block; a NaN score ranks last. A query block without a valid
+ * row gets no key block. Always listed, ahead of any score: blocks
+ * [0, keep_first), and with keep_local > 0 the blocks that hold the positions of
+ * the query block itself and keep_local - 1 more on each side. */
+H3B_API h3b_status h3b_select_blocks(const h3b_sparse_dims* dims, const void* q, const void* k, const int* q_lens,
+                                     const int* kv_lens, int* blocks, int* counts, void* ws, size_t ws_bytes,
+                                     h3b_stream stream);
+
+/* Softmax attention, scaled by 1/sqrt(head_dim), of each query over the valid
+ * keys of its block's listed key blocks:
+ *   o bf16 [B][Lq][n_heads*head_dim]; rows behind q_lens are left as they were.
+ *   absmax fp32 [B*Lq] or NULL: each row's max |o| is max-combined into it
+ *   (zero it first; rows behind q_lens are left as they were).
+ * A query whose list holds no valid key gets o = 0. counts NULL: every list has
+ * topk entries; a count is clamped to [0, topk]. An entry outside [0, nkb) holds
+ * no key; a block listed twice counts its keys twice. */
+H3B_API h3b_status h3b_attention_blocks(const h3b_sparse_dims* dims, const void* q, const void* k, const void* v,
+                                        const int* q_lens, const int* kv_lens, const int* blocks,
+                                        const int* counts, void* o, float* absmax, void* ws, size_t ws_bytes,
+                                        h3b_stream stream);
+
+/* The residual update of a branch whose output is normalised, and the next
+ * branch's norm, in one pass over rows of d channels:
+ *   x_out = bf16(x + alpha * gate * (post_norm(y) * w_post))
+ *   h     = bf16(pre_norm(x_out) * (1 + scale) + shift)
+ *   h_out = h, and q, s = the per-row int8 quantizer of h (as h3b_quantize_rows)
+ * y, x, x_out, h_out bf16 [rows][d]; q int8 [rows][d]; s fp32 [rows].
+ * post_norm, pre_norm: 0 none, 1 RMS (x * rsqrt(mean(x^2) + eps)), 2 LayerNorm
+ * (no affine, biased variance). x_out may be x; otherwise no output may overlap
+ * an input or another output.
+ *   w_post fp32 [d] or NULL (ones). gate, shift, scale: fp32 [d] per item of
+ *   rows_per_item rows, mod_stride floats (a multiple of 4) apart; NULL is gate
+ *   one, shift zero, scale zero. h_out NULL writes no h; q and s are both given
+ *   or both NULL; with none of the three only x_out is written. absmax_zero fp32
+ *   [rows], set to 0, or NULL.
+ *   d a multiple of 8, 8 <= d <= 8192. */
+typedef struct {
+  int rows, d;
+  int rows_per_item, mod_stride;
+  int post_norm, pre_norm;
+  float post_eps, pre_eps, alpha;
+} h3b_residual_norm_dims;
+H3B_API h3b_status h3b_residual_norm(const h3b_residual_norm_dims* dims, const void* y, const float* w_post,
+                                     const float* gate, const void* x, void* x_out, const float* shift,
+                                     const float* scale, void* h_out, int8_t* q, float* s, float* absmax_zero,
+                                     h3b_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,6 +12,7 @@
 //     preceding kernels; activation memory reused by lifetime).
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdlib>
 #include <mutex>
 #include <string>
@@ -888,6 +889,165 @@ h3b_status h3b_gemm_i8_gelu(const int8_t* A, const float* sA, const int8_t* W, c
   GemmArgs a = base_args(M, N, K, di->err);
   a.sA = sA; a.sW = sW; a.bias = bias; a.out = g; a.absmax = absmax;
   H3B_CK(launch_gemm(true, EPI_GELU, A, W, a, di->sms, stream), "gemm_i8_gelu");
+  return H3B_OK;
+}
+
+// ---- selected key blocks, per-token positions, branch norms -----------------
+
+h3b_status h3b_qk_norm_rope(const h3b_qk_dims* dims, const void* qkv, const float* wq, const float* wk,
+                            const float* pos, void* q, void* k, void* v, h3b_stream stream) {
+  cudaStream_t st = stream;
+  if (!dims) return fail(H3B_ERR_ARG, "dims is NULL");
+  const h3b_qk_dims& d = *dims;
+  if (d.B < 0 || d.L < 0 || (long long)d.B * d.L >= (1LL << 31)) return fail(H3B_ERR_SHAPE, "B*L out of range");
+  if (d.head_dim != 64 && d.head_dim != 128) return fail(H3B_ERR_SHAPE, "head_dim must be 64 or 128");
+  if (d.n_heads < 1 || d.n_kv_heads < 1 || d.n_heads > 1024 || d.n_kv_heads > 1024 || d.n_heads + d.n_kv_heads > 1024)
+    return fail(H3B_ERR_SHAPE, "n_heads and n_kv_heads must be >= 1, their sum <= 1024");
+  if (d.rope_t < 0 || d.rope_h < 0 || d.rope_w < 0 || (d.rope_t | d.rope_h | d.rope_w) & 1 ||
+      (long long)d.rope_t + d.rope_h + d.rope_w > d.head_dim)
+    return fail(H3B_ERR_SHAPE, "rope split must be even parts summing to at most head_dim");
+  if (!(d.rope_theta > 0.0f) || !(d.norm_eps >= 0.0f)) return fail(H3B_ERR_ARG, "rope_theta > 0 and norm_eps >= 0");
+  const long long width = (long long)(d.n_heads + 2 * d.n_kv_heads) * d.head_dim;
+  if (d.row_stride < width || d.row_stride % 8 != 0 || d.row_stride > (1LL << 31))
+    return fail(H3B_ERR_SHAPE, "row_stride must be a multiple of 8, at least (n_heads + 2 n_kv_heads) * head_dim");
+  if ((long long)d.B * d.L == 0) return H3B_OK;  // empty problem: nothing to launch
+  if (!qkv || !q || !k || !v) return fail(H3B_ERR_ARG, "NULL pointer");
+  if (!aligned16(qkv) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(wq) || !aligned16(wk) ||
+      !aligned16(pos))
+    return fail(H3B_ERR_ALIGN, "alignment");
+  DeviceInfo* di = nullptr;
+  h3b_status s = device_info(&di);
+  if (s != H3B_OK) return s;
+  QkRopeArgs a{};
+  a.B = d.B; a.L = d.L; a.n_heads = d.n_heads; a.n_kv_heads = d.n_kv_heads; a.head_dim = d.head_dim;
+  a.row_stride = d.row_stride; a.eps = d.norm_eps; a.err = di->err;
+  a.qkv = qkv; a.wq = wq; a.wk = wk; a.pos = pos; a.q = q; a.k = k; a.v = v;
+  // theta^(-2j/r) / pi by repeated multiplication: within 64 * 2^-53 of the power
+  const int part[3] = {d.rope_t, d.rope_h, d.rope_w};
+  int p = 0;
+  for (int ax = 0; ax < 3; ++ax) {
+    const double step = part[ax] ? pow((double)d.rope_theta, -2.0 / part[ax]) : 1.0;
+    double f = 0.31830988618379067154;
+    for (int j = 0; j < part[ax] / 2; ++j, f *= step) a.freq[p++] = f;
+    a.axis_end[ax] = p;
+  }
+  H3B_CK(launch_qk_norm_rope(a, di->sms, st), "qk_norm_rope");
+  return H3B_OK;
+}
+
+// Host checks shared by the block-sparse entry points (no device query).
+static h3b_status check_sparse(const h3b_sparse_dims* dims, int* nqb, int* nkb) {
+  if (!dims) return fail(H3B_ERR_ARG, "dims is NULL");
+  const h3b_sparse_dims& d = *dims;
+  if (d.B < 0 || d.Lq < 0 || d.Lk < 1) return fail(H3B_ERR_SHAPE, "need B >= 0, Lq >= 0, Lk >= 1");
+  if (d.head_dim != 64 && d.head_dim != 128) return fail(H3B_ERR_SHAPE, "head_dim must be 64 or 128");
+  if (d.block_k != 64 && d.block_k != 128) return fail(H3B_ERR_SHAPE, "block_k must be 64 or 128");
+  if (d.n_heads < 1 || d.n_kv_heads < 1 || d.n_heads % d.n_kv_heads != 0)
+    return fail(H3B_ERR_SHAPE, "n_heads must be a multiple of n_kv_heads >= 1");
+  if ((long long)d.B * d.n_heads > 65535) return fail(H3B_ERR_SHAPE, "B * n_heads must be <= 65535");
+  if ((long long)d.B * d.Lq >= (1LL << 31) || (long long)d.B * d.Lk >= (1LL << 31))
+    return fail(H3B_ERR_SHAPE, "too many tokens");
+  *nqb = (int)(((long long)d.Lq + kSparseQueries - 1) / kSparseQueries);
+  *nkb = (int)(((long long)d.Lk + d.block_k - 1) / d.block_k);
+  if (*nkb > 4096) return fail(H3B_ERR_SHAPE, "more than 4096 key blocks");
+  if (d.topk < 1 || d.topk > *nkb) return fail(H3B_ERR_SHAPE, "topk must be in [1, ceil(Lk / block_k)]");
+  if (d.keep_first < 0 || d.keep_local < 0) return fail(H3B_ERR_ARG, "keep_first and keep_local must be >= 0");
+  if (d.keep_first > d.topk || d.keep_local > d.topk) return fail(H3B_ERR_SHAPE, "more blocks kept than topk");
+  const int own = d.keep_local > 0 ? kSparseQueries / d.block_k + 2 * (d.keep_local - 1) : 0;
+  if (d.keep_first + own > d.topk && d.topk < *nkb) return fail(H3B_ERR_SHAPE, "more blocks kept than topk");
+  return H3B_OK;
+}
+
+h3b_status h3b_sparse_workspace_size(const h3b_sparse_dims* dims, size_t* bytes) {
+  int nqb = 0, nkb = 0;
+  h3b_status s = check_sparse(dims, &nqb, &nkb);
+  if (s != H3B_OK) return s;
+  if (!bytes) return fail(H3B_ERR_ARG, "bytes is NULL");
+  *bytes = align256(std::max(select_ws_bytes(dims->B, dims->n_heads, dims->n_kv_heads, dims->head_dim, nqb, nkb),
+                             sparse_attn_ws_bytes(dims->B, dims->n_heads, dims->head_dim, nqb, dims->topk,
+                                                  dims->block_k)));
+  return H3B_OK;
+}
+
+// The workspace's own checks: 256-byte aligned, at least h3b_sparse_workspace_size bytes.
+static h3b_status check_sparse_ws(const h3b_sparse_dims* dims, const void* ws, size_t ws_bytes) {
+  size_t need = 0;
+  h3b_status s = h3b_sparse_workspace_size(dims, &need);
+  if (s != H3B_OK) return s;
+  if (need == 0) return H3B_OK;
+  if (!ws) return fail(H3B_ERR_ARG, "ws is NULL");
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return fail(H3B_ERR_ALIGN, "workspace not 256-byte aligned");
+  if (ws_bytes < need) return fail(H3B_ERR_WORKSPACE, "workspace smaller than h3b_sparse_workspace_size");
+  return H3B_OK;
+}
+
+h3b_status h3b_select_blocks(const h3b_sparse_dims* dims, const void* q, const void* k, const int* q_lens,
+                             const int* kv_lens, int* blocks, int* counts, void* ws, size_t ws_bytes,
+                             h3b_stream stream) {
+  cudaStream_t st = stream;
+  int nqb = 0, nkb = 0;
+  h3b_status s = check_sparse(dims, &nqb, &nkb);
+  if (s != H3B_OK) return s;
+  if (dims->B == 0 || dims->Lq == 0) return H3B_OK;  // empty problem: nothing to launch
+  if (!q || !k || !blocks || !counts) return fail(H3B_ERR_ARG, "NULL pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(blocks) || !aligned16(counts) || !aligned16(q_lens) ||
+      !aligned16(kv_lens))
+    return fail(H3B_ERR_ALIGN, "alignment");
+  if ((s = check_sparse_ws(dims, ws, ws_bytes)) != H3B_OK) return s;
+  DeviceInfo* di = nullptr;
+  if ((s = device_info(&di)) != H3B_OK) return s;
+  SelectArgs a{dims->B, dims->n_heads, dims->n_kv_heads, dims->head_dim, dims->Lq, dims->Lk, dims->block_k, dims->topk,
+               dims->keep_first, dims->keep_local, nqb, nkb, q, k, q_lens, kv_lens, blocks, counts, ws, di->err};
+  H3B_CK(launch_select_blocks(a, di->sms, st), "select_blocks");
+  return H3B_OK;
+}
+
+h3b_status h3b_attention_blocks(const h3b_sparse_dims* dims, const void* q, const void* k, const void* v,
+                                const int* q_lens, const int* kv_lens, const int* blocks, const int* counts, void* o,
+                                float* absmax, void* ws, size_t ws_bytes, h3b_stream stream) {
+  cudaStream_t st = stream;
+  int nqb = 0, nkb = 0;
+  h3b_status s = check_sparse(dims, &nqb, &nkb);
+  if (s != H3B_OK) return s;
+  if (dims->B == 0 || dims->Lq == 0) return H3B_OK;  // empty problem: nothing to launch
+  if (!q || !k || !v || !blocks || !o) return fail(H3B_ERR_ARG, "NULL pointer");
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(blocks) || !aligned16(counts) || !aligned16(o) ||
+      !aligned16(absmax) || !aligned16(q_lens) || !aligned16(kv_lens))
+    return fail(H3B_ERR_ALIGN, "alignment");
+  if ((s = check_sparse_ws(dims, ws, ws_bytes)) != H3B_OK) return s;
+  DeviceInfo* di = nullptr;
+  if ((s = device_info(&di)) != H3B_OK) return s;
+  SparseAttnArgs a{dims->B, dims->n_heads, dims->n_kv_heads, dims->head_dim, dims->Lq, dims->Lk, dims->block_k,
+                   dims->topk, nqb, nkb, q, k, v, q_lens, kv_lens, blocks, counts, o, absmax, ws, di->err};
+  H3B_CK(launch_sparse_attention(a, st), "attention_blocks");
+  return H3B_OK;
+}
+
+h3b_status h3b_residual_norm(const h3b_residual_norm_dims* dims, const void* y, const float* w_post,
+                             const float* gate, const void* x, void* x_out, const float* shift, const float* scale,
+                             void* h_out, int8_t* q, float* s, float* absmax_zero, h3b_stream stream) {
+  cudaStream_t st = stream;
+  if (!dims) return fail(H3B_ERR_ARG, "dims is NULL");
+  const h3b_residual_norm_dims& d = *dims;
+  if (d.rows < 0 || d.d < 8 || d.d % 8 != 0 || d.d > 8192)
+    return fail(H3B_ERR_SHAPE, "need rows >= 0 and d a multiple of 8 in [8, 8192]");
+  if (d.rows_per_item < 1 || d.mod_stride < 0 || d.mod_stride % 4 != 0)
+    return fail(H3B_ERR_ARG, "rows_per_item/mod_stride");
+  if (d.post_norm < 0 || d.post_norm > 2 || d.pre_norm < 0 || d.pre_norm > 2)
+    return fail(H3B_ERR_ARG, "post_norm and pre_norm must be 0 (none), 1 (RMS) or 2 (LayerNorm)");
+  if (!(d.post_eps >= 0.0f) || !(d.pre_eps >= 0.0f)) return fail(H3B_ERR_ARG, "eps must be >= 0");
+  if (d.rows == 0) return H3B_OK;  // empty problem: nothing to launch
+  if (!y || !x || !x_out || (q != nullptr) != (s != nullptr)) return fail(H3B_ERR_ARG, "NULL pointer");
+  if (!aligned16(y) || !aligned16(w_post) || !aligned16(gate) || !aligned16(x) || !aligned16(x_out) ||
+      !aligned16(shift) || !aligned16(scale) || !aligned16(h_out) || !aligned16(q) || !aligned16(s) ||
+      !aligned16(absmax_zero))
+    return fail(H3B_ERR_ALIGN, "alignment");
+  DeviceInfo* di = nullptr;
+  h3b_status hs = device_info(&di);
+  if (hs != H3B_OK) return hs;
+  ResNormArgs a{d.rows, d.d, d.rows_per_item, d.mod_stride, d.post_norm, d.pre_norm, d.post_eps, d.pre_eps, d.alpha,
+                y, x, w_post, gate, shift, scale, x_out, h_out, q, s, absmax_zero, di->err};
+  H3B_CK(launch_residual_norm(a, di->sms, st), "residual_norm");
   return H3B_OK;
 }
 

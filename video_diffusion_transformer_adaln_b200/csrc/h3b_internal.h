@@ -80,6 +80,60 @@ struct AttnArgs {
 };
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t st);
 
+// ---- per-head norm and per-token rotary positions (k_qk_rope.cu)
+struct QkRopeArgs {
+  int B, L, n_heads, n_kv_heads, head_dim;
+  long long row_stride;
+  const void* qkv;
+  const float *wq, *wk, *pos;
+  void *q, *k, *v;
+  float eps;
+  int axis_end[3];   // first pair after each axis's part (t, h, w)
+  double freq[64];   // half turns per unit position of each rotated pair
+  unsigned* err;
+};
+cudaError_t launch_qk_norm_rope(const QkRopeArgs& a, int sms, cudaStream_t st);
+
+// ---- selection of key blocks (k_select.cu) and attention over them (k_sparse_attention.cu)
+constexpr int kSparseQueries = 128;  // queries per block
+struct SelectArgs {
+  int B, n_heads, n_kv_heads, head_dim, Lq, Lk, block_k, topk, keep_first, keep_local;
+  int nqb, nkb;
+  const void *q, *k;
+  const int *q_lens, *kv_lens;
+  int *blocks, *counts;
+  void* ws;
+  unsigned* err;
+};
+size_t select_ws_bytes(int B, int n_heads, int n_kv_heads, int head_dim, int nqb, int nkb);
+cudaError_t launch_select_blocks(const SelectArgs& a, int sms, cudaStream_t st);
+
+struct SparseAttnArgs {
+  int B, n_heads, n_kv_heads, head_dim, Lq, Lk, block_k, topk;
+  int nqb, nkb;
+  const void *q, *k, *v;
+  const int *q_lens, *kv_lens, *blocks, *counts;
+  void* o;
+  float* absmax;
+  void* ws;
+  unsigned* err;
+};
+size_t sparse_attn_ws_bytes(int B, int n_heads, int head_dim, int nqb, int topk, int block_k);
+cudaError_t launch_sparse_attention(const SparseAttnArgs& a, cudaStream_t st);
+
+// ---- gated residual with norms on both sides (k_resnorm.cu)
+struct ResNormArgs {
+  int rows, d, rows_per_item, mod_stride, post_norm, pre_norm;
+  float post_eps, pre_eps, alpha;
+  const void *y, *x;
+  const float *w_post, *gate, *shift, *scale;
+  void *x_out, *h_out;
+  int8_t* q;
+  float *s, *absmax_zero;
+  unsigned* err;
+};
+cudaError_t launch_residual_norm(const ResNormArgs& a, int sms, cudaStream_t st);
+
 // ---- error detail reported by h3b_last_error_detail (h3b_api.cu)
 void set_error_detail(const std::string& why);
 // ---- H3B_OK when the current device is compute capability 10.0, else the status

@@ -36,7 +36,7 @@
 // warp-collective TMEM access is warp-uniform.
 #include "h3b_common.cuh"
 #include "h3b_internal.h"
-
+#include "h3b_softmax.cuh"
 
 namespace h3b {
 namespace attn {
@@ -48,44 +48,6 @@ constexpr uint32_t kRegsControl = 56, kRegsSoftmax = 224;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int BOX = 16384;  // one TMA box: 128 rows x 128 bytes
 }  // namespace attn
-
-__device__ __forceinline__ float fast_exp2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// 2^x on the FMA pipe, two lanes at a time: x = n + f with n = round(x) and
-// f in [-1/2, 1/2]; 2^f by a cubic fitted here for minimax relative error on
-// that interval (Remez exchange; max relative error 7.5e-5, below the 2^-9 of
-// the bf16 rounding that P then goes through), and 2^n added to the exponent
-// field. Adding 1.5 * 2^23 rounds x to an integer held in the low mantissa
-// bits; x is clamped at -125 so that 2^n stays a normal number.
-constexpr float kExp2C0 = 0.99992806f, kExp2C1 = 0.69326097f, kExp2C2 = 0.24261113f, kExp2C3 = 0.05517167f;
-__device__ __forceinline__ float2 exp2_poly2(float2 x) {
-  x = make_float2(fmaxf(x.x, -125.0f), fmaxf(x.y, -125.0f));
-  const float2 t = __fadd2_rn(x, make_float2(12582912.0f, 12582912.0f));
-  const float2 r = __fadd2_rn(t, make_float2(-12582912.0f, -12582912.0f));
-  const float2 f = __ffma2_rn(r, make_float2(-1.0f, -1.0f), x);
-  float2 p = __ffma2_rn(make_float2(kExp2C3, kExp2C3), f, make_float2(kExp2C2, kExp2C2));
-  p = __ffma2_rn(p, f, make_float2(kExp2C1, kExp2C1));
-  p = __ffma2_rn(p, f, make_float2(kExp2C0, kExp2C0));
-  return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                     __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
-}
-__device__ __forceinline__ float max3f(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-// tcgen05.mma with the A operand in tensor memory (kind::f16, bf16 inputs).
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 
 template <int DH>
 struct AttnLayout {

@@ -52,6 +52,31 @@ class KernelTime(C.Structure):
     _fields_ = [("name", C.c_char_p), ("launches", C.c_int), ("total_ms", C.c_double)]
 
 
+class QkDims(C.Structure):
+    _fields_ = [("B", C.c_int), ("L", C.c_int), ("n_heads", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("rope_t", C.c_int), ("rope_h", C.c_int), ("rope_w", C.c_int),
+                ("rope_theta", C.c_float), ("norm_eps", C.c_float), ("row_stride", C.c_longlong)]
+
+
+class SparseDims(C.Structure):
+    _fields_ = [(n, C.c_int) for n in ("B", "n_heads", "n_kv_heads", "head_dim", "Lq", "Lk", "block_k", "topk",
+                                       "keep_first", "keep_local")]
+
+    @property
+    def nqb(self) -> int:
+        return -(-self.Lq // 128)
+
+    @property
+    def nkb(self) -> int:
+        return -(-self.Lk // self.block_k)
+
+
+class ResidualNormDims(C.Structure):
+    _fields_ = [("rows", C.c_int), ("d", C.c_int), ("rows_per_item", C.c_int), ("mod_stride", C.c_int),
+                ("post_norm", C.c_int), ("pre_norm", C.c_int),
+                ("post_eps", C.c_float), ("pre_eps", C.c_float), ("alpha", C.c_float)]
+
+
 _LIB = None
 
 
@@ -100,6 +125,11 @@ def _declare(L):
         "h3b_range_delta": [vp, vp, vp, C.c_longlong, vp],
         "h3b_range_apply": [vp, vp, C.c_longlong, vp],
         "h3b_gemm_i8_gelu": [vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, vp],
+        "h3b_qk_norm_rope": [vp, vp, vp, vp, vp, vp, vp, vp, vp],
+        "h3b_sparse_workspace_size": [vp, C.POINTER(sz)],
+        "h3b_select_blocks": [vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "h3b_attention_blocks": [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "h3b_residual_norm": [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp],
     }
     for name, args in sigs.items():
         f = getattr(L, name)
@@ -352,6 +382,56 @@ def h3b_gemm_i8_gelu(A, sA, W, sW, bias, g, absmax, stream=None):
     N = W.shape[0]
     _check(lib().h3b_gemm_i8_gelu(_p(A), _p(sA), _p(W), _p(sW), _p(bias), _p(g), _p(absmax), M, N, K, _s(stream)),
            "h3b_gemm_i8_gelu")
+
+
+# --------------------------------------------------------------------------- selected blocks, branch norms
+
+def make_qk(B, L, n_heads, n_kv_heads, head_dim, rope, rope_theta=10000.0, norm_eps=1e-6, row_stride=None) -> QkDims:
+    """row_stride defaults to the projection's own width (no padding columns)."""
+    width = (n_heads + 2 * n_kv_heads) * head_dim
+    return QkDims(B, L, n_heads, n_kv_heads, head_dim, rope[0], rope[1], rope[2], rope_theta, norm_eps,
+                  width if row_stride is None else row_stride)
+
+
+def h3b_qk_norm_rope(dims: QkDims, qkv, wq, wk, pos, q, k, v, stream=None):
+    _check(lib().h3b_qk_norm_rope(C.byref(dims), _p(qkv), _p(wq), _p(wk), _p(pos), _p(q), _p(k), _p(v), _s(stream)),
+           "h3b_qk_norm_rope")
+
+
+def make_sparse(B, n_heads, n_kv_heads, head_dim, Lq, Lk, block_k, topk, keep_first=0, keep_local=0) -> SparseDims:
+    return SparseDims(B, n_heads, n_kv_heads, head_dim, Lq, Lk, block_k, topk, keep_first, keep_local)
+
+
+def h3b_sparse_workspace_size(dims: SparseDims) -> int:
+    n = C.c_size_t(0)
+    _check(lib().h3b_sparse_workspace_size(C.byref(dims), C.byref(n)), "h3b_sparse_workspace_size")
+    return n.value
+
+
+def h3b_select_blocks(dims: SparseDims, q, k, q_lens, kv_lens, blocks, counts, ws, stream=None):
+    _check(lib().h3b_select_blocks(C.byref(dims), _p(q), _p(k), _p(q_lens), _p(kv_lens), _p(blocks), _p(counts),
+                                   _p(ws), ws.numel() * ws.element_size(), _s(stream)), "h3b_select_blocks")
+
+
+def h3b_attention_blocks(dims: SparseDims, q, k, v, q_lens, kv_lens, blocks, counts, o, absmax, ws, stream=None):
+    _check(lib().h3b_attention_blocks(C.byref(dims), _p(q), _p(k), _p(v), _p(q_lens), _p(kv_lens), _p(blocks),
+                                      _p(counts), _p(o), _p(absmax), _p(ws), ws.numel() * ws.element_size(),
+                                      _s(stream)), "h3b_attention_blocks")
+
+
+NORMS = {"none": 0, "rms": 1, "layer": 2}
+
+
+def make_residual_norm(rows, d, rows_per_item, mod_stride, post="rms", pre="layer", post_eps=1e-6, pre_eps=1e-6,
+                       alpha=1.0) -> ResidualNormDims:
+    """post, pre: "none", "rms" or "layer"."""
+    return ResidualNormDims(rows, d, rows_per_item, mod_stride, NORMS[post], NORMS[pre], post_eps, pre_eps, alpha)
+
+
+def h3b_residual_norm(dims: ResidualNormDims, y, w_post, gate, x, x_out, shift, scale, h_out=None, q=None, s=None,
+                      absmax_zero=None, stream=None):
+    _check(lib().h3b_residual_norm(C.byref(dims), _p(y), _p(w_post), _p(gate), _p(x), _p(x_out), _p(shift), _p(scale),
+                                   _p(h_out), _p(q), _p(s), _p(absmax_zero), _s(stream)), "h3b_residual_norm")
 
 
 # --------------------------------------------------------------------------- profiling
