@@ -208,3 +208,22 @@ def test_workspace_size_is_enough():
     o = torch.full((B, Lq, H * dh), 9.0, dtype=torch.bfloat16, device="cuda")
     h3b.h3b_attention_blocks(d, q, k, v, None, None, blocks, counts, o, None, buf[:need])
     assert torch.equal(o, want) and (buf[need:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("Lq", [200, 1])
+def test_a_bad_key_reaches_every_query_that_lists_it(value, Lq):
+    """A NaN or infinite score makes the formula's row NaN, wherever in its tile the key lies."""
+    require_gpu()
+    B, H, dh, Lk = 1, 1, 128, 3000
+    nqb, nkb = -(-Lq // 128), 47
+    q, v = randn((B, H, Lq, dh), 36).abs(), randn((B, H, Lk, dh), 37)
+    blocks, _ = lists(B, H, nqb, nkb, 20, 38)
+    blocks[0, 0, 0, 7] = int(blocks[0, 0, 0, 6])
+    bad = int(blocks[0, 0, 0, 7])
+    for lane in (0, 6, 7, 63):
+        k = randn((B, H, Lk, dh), 39)
+        k[0, 0, min(bad * 64 + lane, Lk - 1)] = value
+        o, _, _ = run(q, k, v, blocks, None, 64)
+        has = (blocks[0, 0] == bad).any(-1).repeat_interleave(128)[:Lq]
+        assert o[0, has].isnan().all() and o[0, ~has].isfinite().all()

@@ -949,6 +949,7 @@ static h3b_status check_sparse(const h3b_sparse_dims* dims, int* nqb, int* nkb) 
     return fail(H3B_ERR_SHAPE, "too many tokens");
   *nqb = (int)(((long long)d.Lq + kSparseQueries - 1) / kSparseQueries);
   *nkb = (int)(((long long)d.Lk + d.block_k - 1) / d.block_k);
+  if ((long long)d.B * d.n_heads * *nqb >= (1LL << 31)) return fail(H3B_ERR_SHAPE, "too many query blocks");
   if (*nkb > 4096) return fail(H3B_ERR_SHAPE, "more than 4096 key blocks");
   if (d.topk < 1 || d.topk > *nkb) return fail(H3B_ERR_SHAPE, "topk must be in [1, ceil(Lk / block_k)]");
   if (d.keep_first < 0 || d.keep_local < 0) return fail(H3B_ERR_ARG, "keep_first and keep_local must be >= 0");
