@@ -227,3 +227,20 @@ def test_a_bad_key_reaches_every_query_that_lists_it(value, Lq):
         o, _, _ = run(q, k, v, blocks, None, 64)
         has = (blocks[0, 0] == bad).any(-1).repeat_interleave(128)[:Lq]
         assert o[0, has].isnan().all() and o[0, ~has].isfinite().all()
+
+
+@pytest.mark.parametrize("dh,block_k,kv_lens", [(128, 64, None), (64, 64, [1900, 777, 64]), (128, 64, [1999, 130, 1]),
+                                                (128, 128, [1500, 2000, 0])])
+def test_more_pairs_of_query_blocks_than_processors(dh, block_k, kv_lens):
+    """Lists of every length, empty ones among them, on CTAs that work on several pairs in turn."""
+    require_gpu()
+    B, H, KV, Lq, Lk = 3, 32, 8, 1024, 2000
+    q, k, v = randn((B, H, Lq, dh), 40), randn((B, KV, Lk, dh), 41), randn((B, KV, Lk, dh), 42)
+    nkb = -(-Lk // block_k)
+    blocks, counts = lists(B, H, 8, nkb, nkb, 43)
+    if kv_lens:
+        for b in range(B):
+            k[b, :, kv_lens[b]:] = float("nan")
+            v[b, :, kv_lens[b]:] = float("nan")
+    check(q, k, v, blocks, counts, block_k, None, kv_lens)
+    check(q, k, v, blocks[..., :3].contiguous(), None, block_k, [1024, 1000, 1], kv_lens)

@@ -4,16 +4,20 @@
 // in one pass over each list with the running maximum and sum of the softmax.
 //
 // An item is a query block of one head with a range of its list, 128 listed keys
-// (a tile: two units of 64, gathered by their own TMA loads) at a time. One CTA
-// works on two items, each with its own list, so that one item's products fill
-// the tensor core while the other's softmax runs:
-//   warp 0     TMA: Q of both items, then the K and V tiles of both lists in the
-//              order the MMAs use them, into one ring of slots
-//   warp 1     tcgen05.mma from one thread, in the order
-//                S0(0) S1(0) | PV0(0) S0(1) PV1(0) S1(1) | PV0(1) S0(2) ...
-//              where an item whose list has ended drops out
-//   warps 2-3  idle (they complete warpgroup 0 for the register split)
-//   warps 4-7  softmax of item 0, warps 8-11 softmax of item 1 (thread = row)
+// (a tile: two units of 64, gathered by their own TMA loads) at a time. A CTA
+// works on pairs of items, each item with its own list, so that one item's
+// products fill the tensor core while the other's softmax runs:
+//   warps 0, 2  TMA for item 0, 1: Q, then the K and V tiles, each into its place
+//               in one ring of slots that all loads share in the order of the MMAs
+//   warp 1      tcgen05.mma from one thread, in the order
+//                 S0(0) S1(0) | PV0(0) S0(1) PV1(0) S1(1) | PV0(1) S0(2) ...
+//               where an item whose list has ended drops out
+//   warp 3      the next pair: takes over a CTA of this grid that has not started
+//               (clusterlaunchcontrol), reads what its items need into shared
+//               memory, and looks through their lists
+//   warps 4-7   softmax of item 0, warps 8-11 softmax of item 1 (thread = row)
+// The grid has one CTA per pair; the CTAs that run take over the others, so that
+// the loads and first products of a pair overlap the end of the pair before it.
 // A warp without a valid query row does no softmax (one new token uses one of
 // four). Tensor memory (512 columns): S0 | S1 | O0 | O1; P_g overwrites the first
 // half of S_g. When S_g(j) is complete, PV_g(j-1) is too (a commit tracks every
@@ -46,6 +50,8 @@ constexpr uint32_t kRegsControl = 56, kRegsSoftmax = 224;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kUnitBox = kUnit * 128;  // bytes of 64 rows x 64 lanes
 constexpr int kBox = kTile * 128;      // bytes of 128 rows x 64 lanes
+constexpr int kPairs = 2;              // pairs of items in flight in a CTA
+constexpr int kItemBytes = 64;
 constexpr float kNoMax = -3.0e38f;     // running maximum before any key
 
 struct SparseParams {
@@ -63,8 +69,14 @@ struct Layout {
   static constexpr int NS = DH == 128 ? 5 : 10;
   static constexpr int Q_OFF = 0, RING_OFF = 2 * TILE;
   static constexpr int BAR_OFF = RING_OFF + NS * TILE;
-  static constexpr int NBARS = 2 + 2 * NS + 6 + 1;
-  static constexpr size_t SMEM = (size_t)BAR_OFF + NBARS * 8 + 16 + 1024;
+  // mbarriers, by their place: per item (two each), per slot, per pair in flight
+  static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 6, FIN = 8, FULL = 10, EMPTY = FULL + NS;
+  static constexpr int PAIR_FULL = EMPTY + NS, PAIR_EMPTY = PAIR_FULL + kPairs, CANCEL = PAIR_EMPTY + kPairs;
+  static constexpr int DRAIN = CANCEL + 1, NBARS = DRAIN + 1;
+  static constexpr int FLAG_OFF = BAR_OFF + (NBARS + 1) / 2 * 16;  // tensor memory address, abort flag, loads
+  static constexpr int RESPONSE_OFF = FLAG_OFF + 16;               // of the take-over request
+  static constexpr int ITEM_OFF = RESPONSE_OFF + 16;               // [kPairs][2]
+  static constexpr size_t SMEM = (size_t)ITEM_OFF + kPairs * 2 * kItemBytes + 1024;
   static constexpr uint32_t S_COL(int g) { return g * 128u; }
   static constexpr uint32_t O_COL(int g) { return 256u + g * DH; }
 };
@@ -81,19 +93,30 @@ __device__ __forceinline__ int clamp_len(const int* lens, int b, int L) {
   return lens ? min(max(__ldg(lens + b), 0), L) : L;
 }
 
-// What an item works on; the same in every thread.
-struct Item {
-  int bh, qb;      // batch item x head, query block
-  int kvrow;       // batch item x key head
-  int qn, kn;      // valid queries and keys of the batch item
-  int t0, units;   // first tile of the range, units in it
-  int tiles;       // ceil(units / 2)
-  const int* list;
-  int entries;     // list entries in use
-  bool rows;       // holds valid query rows
-};
+// A descriptor whose start address lies `units` of 16 bytes further: the address field is in the low
+// half and does not overflow within shared memory. The volatile add keeps the sums from being kept in
+// registers for every step of every product, which spills.
+__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t units) {
+  uint32_t lo = (uint32_t)d, r;
+  asm volatile("add.u32 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(units));
+  return (d & 0xFFFFFFFF00000000ull) | r;
+}
 
-__device__ __forceinline__ Item load_item(const SparseParams& p, int item) {
+// What an item works on. Kept in shared memory: the softmax threads' registers are the scores'.
+struct Item {
+  int bh, qb;     // batch item x head, query block
+  int kvrow;      // batch item x key head
+  int qn, kn;     // valid queries and keys of the batch item
+  int t0, units;  // first tile of the range, units in it
+  int tiles;      // ceil(units / 2); -1: no further pair
+  int clean;      // every unit of the range holds 64 valid keys
+  int pad;
+  const int* list;
+};
+static_assert(sizeof(Item) <= kItemBytes && kItemBytes % 8 == 0, "the items' place in shared memory");
+
+// By a whole warp.
+__device__ __forceinline__ Item load_item(const SparseParams& p, int item, int lane) {
   const SparseAttnArgs& a = p.a;
   Item it{};
   if (item >= p.rows * p.nsplit) return it;
@@ -104,46 +127,108 @@ __device__ __forceinline__ Item load_item(const SparseParams& p, int item) {
   it.kvrow = b * a.n_kv_heads + h / (a.n_heads / a.n_kv_heads);
   it.qn = clamp_len(a.q_lens, b, a.Lq);
   it.kn = clamp_len(a.kv_lens, b, a.Lk);
-  it.rows = it.qb * kSparseQueries < it.qn;
   it.list = a.blocks + (size_t)row * a.topk;
-  it.entries = a.counts ? min(max(__ldg(a.counts + row), 0), a.topk) : a.topk;
-  const int all = it.rows && it.kn > 0 ? it.entries * (a.block_k / kUnit) : 0;
+  const int entries = a.counts ? min(max(__ldg(a.counts + row), 0), a.topk) : a.topk;
+  const int per = a.block_k / kUnit;  // units per entry
+  const int all = it.qb * kSparseQueries < it.qn && it.kn > 0 ? entries * per : 0;
   it.t0 = split * p.split_tiles;
   it.units = min(max(all - 2 * it.t0, 0), 2 * p.split_tiles);
   it.tiles = (it.units + 1) / 2;
+  bool clean = true;
+  for (int u = lane * per; u < it.units; u += 32 * per) {
+    const int v = __ldg(it.list + (2 * it.t0 + u) / per);
+    clean = clean && (unsigned)v < (unsigned)a.nkb && (v + 1) * a.block_k <= it.kn;
+  }
+  it.clean = __all_sync(0xFFFFFFFFu, clean);
   return it;
 }
 
-// Walks an item's list in tiles; a warp's lanes hold 32 entries, with the next 32 on their way.
+// Walks an item's list in tiles; a warp's lanes hold 32 entries as the first keys of their blocks
+// (`none` where an entry holds no valid key), with the next 32 on their way.
 struct ListWalk {
-  int cur, nxt, base;  // this lane's entry of the chunk that starts at entry `base`, and of the next
-  __device__ __forceinline__ static int fetch(const Item& it, int e) {
-    return e < it.entries ? __ldg(it.list + e) : -1;
+  const int* list;
+  int entries, kn, block_k, nkb, none;  // entries: of the range
+  int cur, nxt, base;                   // this lane's entry of the chunk that starts at entry `base`, and of the next
+  __device__ __forceinline__ int fetch(int e) const {
+    const int v = e < entries ? __ldg(list + e) : -1;
+    return (unsigned)v < (unsigned)nkb && v * block_k < kn ? v * block_k : none;
   }
-  __device__ __forceinline__ void start(const Item& it, int per_tile, int lane) {
-    base = it.t0 * per_tile & ~31;
-    cur = fetch(it, base + lane);
-    nxt = fetch(it, base + 32 + lane);
-  }
-  // First keys of the two units of tile t (from the item's first): `none` where a unit holds no valid key.
-  __device__ __forceinline__ int2 tile(const Item& it, int t, int block_k, int nkb, int none, int lane) {
+  // First keys of the two units of tile t of a list whose last unit is `units` - 1.
+  __device__ __forceinline__ int2 tile(int t, int units, int lane) {
     const bool wide = block_k == kTile;
-    const int e0 = wide ? it.t0 + t : 2 * (it.t0 + t);
+    const int e0 = wide ? t : 2 * t;
     if (e0 - base >= 32) {
       base += 32;
       cur = nxt;
-      nxt = fetch(it, base + 32 + lane);
+      nxt = fetch(base + 32 + lane);
     }
-    const int a = __shfl_sync(0xFFFFFFFFu, cur, e0 - base);
-    const int b = wide ? a : __shfl_sync(0xFFFFFFFFu, cur, e0 - base + 1);
     int2 s;
-    s.x = (unsigned)a < (unsigned)nkb ? a * block_k : none;
-    s.y = (unsigned)b < (unsigned)nkb ? b * block_k + (wide ? kUnit : 0) : none;
-    if (s.x >= it.kn) s.x = none;
-    if (s.y >= it.kn || 2 * t + 1 >= it.units) s.y = none;
+    s.x = __shfl_sync(0xFFFFFFFFu, cur, e0 - base);
+    s.y = __shfl_sync(0xFFFFFFFFu, cur, e0 - base + (wide ? 0 : 1));
+    if (wide) s.y = s.x + kUnit < kn ? s.x + kUnit : none;
+    if (2 * t + 1 >= units) s.y = none;
     return s;
   }
 };
+
+// A place in the order of loads: its slot in the ring, the parity of that use of the slot, its number.
+template <int NS>
+struct Place {
+  int slot = 0;
+  uint32_t ph = 0, n = 0;
+  __device__ __forceinline__ void advance(int by) {  // by <= NS
+    n += by;
+    slot += by;
+    if (slot >= NS) {
+      slot -= NS;
+      ph ^= 1u;
+    }
+  }
+  __device__ __forceinline__ void advance_any(int by) {
+    n += by;
+    const int s = slot + by;
+    ph ^= (uint32_t)(s / NS) & 1u;
+    slot = s % NS;
+  }
+};
+
+// Waits (a whole warp, which decides as one) until *count, a running number, has reached `n`; bounded
+// like every wait of the library.
+__device__ __forceinline__ bool wait_reached(const volatile uint32_t* count, uint32_t n, const volatile int* abort,
+                                             unsigned* err) {
+  const uint64_t t0 = globaltimer();
+  for (uint32_t i = 1;; ++i) {
+    if (__all_sync(0xFFFFFFFFu, (int32_t)(*count - n) >= 0)) return true;
+    if ((i & 63u) != 0) continue;
+    const bool late = globaltimer() - t0 > kWaitLimitNs;
+    if (__any_sync(0xFFFFFFFFu, late || *abort)) {
+      if (late) atomicOr(err, ERR_WAIT_MMA);
+      return false;
+    }
+  }
+}
+
+// Asks for the takeover of a CTA of this grid that has not started; the 16-byte response completes on `bar`.
+__device__ __forceinline__ void request_cta(uint32_t response, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   response),
+               "r"(bar)
+               : "memory");
+}
+// blockIdx.x of the CTA taken over, or -1 when none was left.
+__device__ __forceinline__ int taken_cta(uint32_t response) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(response)
+      : "memory");
+  return ok ? (int)x : -1;
+}
 
 template <int DH, int kPolyMod>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -154,194 +239,271 @@ __global__ void __launch_bounds__(kThreads, 1)
   const SparseAttnArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sb0 = smem_u32(smem);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
-  const uint32_t bar0 = smem_u32(bars);
-  auto q_full = [&](int g) { return bar0 + 8u * g; };
-  auto full = [&](int s) { return bar0 + 8u * (2 + s); };
-  auto empty = [&](int s) { return bar0 + 8u * (2 + NS + s); };
-  auto s_full = [&](int g) { return bar0 + 8u * (2 + 2 * NS + g); };
-  auto p_full = [&](int g) { return bar0 + 8u * (4 + 2 * NS + g); };
-  auto fin = [&](int g) { return bar0 + 8u * (6 + 2 * NS + g); };
-  const uint32_t drain = bar0 + 8u * (8 + 2 * NS);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + Lay::NBARS);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t sb = smem_u32(smem);
+  auto bar = [&](int place) { return sb + Lay::BAR_OFF + 8u * place; };
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Lay::FLAG_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::FLAG_OFF + 4);
+  volatile uint32_t* loaded = reinterpret_cast<volatile uint32_t*>(smem + Lay::FLAG_OFF + 8);  // each producer's last load
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr uint32_t IDESC_S = instr_desc(1, 1, 0, 0, kSparseQueries, kTile);
   constexpr uint32_t IDESC_S_HALF = instr_desc(1, 1, 0, 0, kSparseQueries, kUnit);
   constexpr uint32_t IDESC_PV = instr_desc(1, 1, 0, 1, kSparseQueries, DH);
 
   if (threadIdx.x == 0) {
-    for (int g = 0; g < 2; ++g) {
-      mbar_init(q_full(g), 1); mbar_init(s_full(g), 1); mbar_init(p_full(g), 4); mbar_init(fin(g), 1);
-    }
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
-    }
-    mbar_init(drain, 1);
+    for (int i = 0; i < Lay::NBARS; ++i) mbar_init(bar(i), 1);
+    for (int g = 0; g < 2; ++g) mbar_init(bar(Lay::P_FULL + g), 4);                  // softmax warps of an item
+    for (int i = 0; i < kPairs; ++i) mbar_init(bar(Lay::PAIR_EMPTY + i), 2 + 1 + 8);  // producers, MMA, softmax warps
     *abort_flag = 0;
+    loaded[0] = loaded[1] = ~0u;
     fence_barrier_init();
-  }
-  if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&tmq);
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_alloc(sb + Lay::FLAG_OFF, kTmemCols);
     tmem_relinquish();
     tc_fence_before();
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   griddep_wait();  // q, k, v and the lists may be the previous grid's output
   griddep_launch_dependents();
 
-  const int none = a.nkb * a.block_k;  // >= Lk: rows there read as zeros
-  const int per_tile = kTile / a.block_k;
+  // Pair k of this CTA, in every role: its items once they are there (nullptr after a failure).
+  // `lanes`: those that call it, which decide as one (they may see the abort flag at different times).
+  auto pair_items = [&](int k, unsigned lanes) -> const Item* {
+    const bool ok = mbar_wait_or_abort(bar(Lay::PAIR_FULL + k % kPairs), (k / kPairs) & 1, abort_flag, a.err, ERR_WAIT_EPI);
+    if (!__all_sync(lanes, ok)) return nullptr;
+    return reinterpret_cast<const Item*>(smem + Lay::ITEM_OFF + (k % kPairs) * 2 * kItemBytes);
+  };
+  auto second = [](const Item* it) {
+    return reinterpret_cast<const Item*>(reinterpret_cast<const uint8_t*>(it) + kItemBytes);
+  };
+
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
-    if (warp == 0) {
-      // ---------------- TMA producer (whole warp; lane 0 issues)
-      const Item it[2] = {load_item(p, 2 * blockIdx.x), load_item(p, 2 * blockIdx.x + 1)};
-      ListWalk walk[2];
-      int2 at[2];  // the units of the K tile loaded last, for its V tile
+    if (warp == 0 || warp == 2) {
+      // ---------------- TMA producer of item g (whole warp; lane 0 issues)
+      const int g = warp >> 1;
+      Place<NS> place;                  // of the pair's first load
+      uint32_t last = ~0u;              // number of this warp's load before; none yet: the one before the first
+      uint32_t filled = 0, phases = 0;  // slots this warp has filled, with the parity of the last use
+      uint32_t items_done = 0;          // items with keys so far
       bool ok = true;
-      int slot = 0, used = 0;  // used: loads issued
-      uint32_t ph = 0;
-      auto load = [&](const CUtensorMap* tm, int g, int t) -> bool {
-        if (used >= NS) {  // the warp decides as one: its lanes may see the abort flag at different times
-          const bool free_ = mbar_wait_or_abort(empty(slot), ph ^ 1u, abort_flag, a.err, ERR_WAIT_MMA);
-          if (!__all_sync(0xFFFFFFFFu, free_)) return false;
+      auto load = [&](const CUtensorMap* map, Place<NS> at, int2 keys, bool two, int kvrow) -> bool {
+        // Wait until the slot's use before this one is released. A parity tells two uses apart, not
+        // more, so the use before that must be known to be over: it is once a load at most NS places
+        // back has waited (slots are released in order), this warp's own or, where the other item has
+        // had more loads since, the other warp's.
+        if (at.n - last > NS && !wait_reached(&loaded[g ^ 1], at.n - NS, abort_flag, a.err)) return false;
+        const bool free_ = mbar_wait_or_abort(bar(Lay::EMPTY + at.slot), at.ph ^ 1u, abort_flag, a.err, ERR_WAIT_MMA);
+        if (!__all_sync(0xFFFFFFFFu, free_)) return false;
+        last = at.n;
+        if (lane == 0) loaded[g] = at.n;
+        filled |= 1u << at.slot;
+        phases = (phases & ~(1u << at.slot)) | (at.ph << at.slot);
+        if (lane == 0) {
+          const uint32_t full = bar(Lay::FULL + at.slot);
+          const uint32_t dst = sb + Lay::RING_OFF + at.slot * Lay::TILE;
+          mbar_arrive_expect_tx(full, (two ? 2 : 1) * Lay::NBOX * kUnitBox);
+#pragma unroll
+          for (int b = 0; b < Lay::NBOX; ++b) {
+            tma_load_3d(dst + b * kBox, map, full, b * 64, keys.x, kvrow);
+            if (two) tma_load_3d(dst + b * kBox + kUnitBox, map, full, b * 64, keys.y, kvrow);
+          }
+        }
+        return true;
+      };
+      for (int k = 0; ok; ++k) {
+        const Item* pair = pair_items(k, 0xFFFFFFFFu);
+        if (!pair) { ok = false; break; }
+        const int n0 = pair->tiles, n1 = second(pair)->tiles;
+        if (n0 < 0) break;
+        const Item* it = g ? second(pair) : pair;
+        const int n = g ? n1 : n0, units = it->units, kvrow = it->kvrow;
+        Place<NS> at = place;
+        place.advance_any(2 * (n0 + n1));
+        if (n > 0) {
+          ListWalk walk;
+          walk.block_k = a.block_k;
+          walk.nkb = a.nkb;
+          walk.none = a.nkb * a.block_k;  // >= Lk: rows there read as zeros
+          walk.kn = it->kn;
+          walk.list = it->list + (a.block_k == kTile ? it->t0 : 2 * it->t0);
+          walk.entries = a.block_k == kTile ? (units + 1) / 2 : units;
+          walk.base = 0;
+          walk.cur = walk.fetch(lane);
+          walk.nxt = walk.fetch(32 + lane);
+          // Q, once the item before is done with its S products
+          if (items_done > 0) {
+            const bool free_ =
+                mbar_wait_or_abort(bar(Lay::Q_EMPTY + g), (items_done - 1) & 1, abort_flag, a.err, ERR_WAIT_MMA);
+            if (!__all_sync(0xFFFFFFFFu, free_)) { ok = false; break; }
+          }
+          ++items_done;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(bar(Lay::Q_FULL + g), Lay::TILE);
+#pragma unroll
+            for (int b = 0; b < Lay::NBOX; ++b)
+              tma_load_3d(sb + Lay::Q_OFF + g * Lay::TILE + b * kBox, &tmq, bar(Lay::Q_FULL + g), b * 64,
+                          it->qb * kSparseQueries, it->bh);
+          }
+          if (g == 1) at.advance(n0 > 0);
+          int2 keys = walk.tile(0, units, lane);
+          ok = load(&tmk, at, keys, units > 1, kvrow);
+          // to this item's first load of round 0: past the other item's first K tile (item 0) or its
+          // loads of the round (item 1)
+          at.advance(1 + (g == 0 ? (n1 > 0) : (n0 > 0) + (n0 > 1)));
+          for (int t = 0; t < n && ok; ++t) {
+            ok = load(&tmv, at, keys, units - 2 * t > 1, kvrow);
+            if (!ok || t + 1 == n) break;
+            at.advance(1);
+            keys = walk.tile(t + 1, units, lane);
+            ok = load(&tmk, at, keys, units - 2 * (t + 1) > 1, kvrow);
+            // past the other item's loads between: the rest of round t (item 0) or the start of round t + 1 (item 1)
+            at.advance(1 + (g == 0 ? (t < n1) + (t + 1 < n1) : (t + 1 < n0) + (t + 2 < n0)));
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Lay::PAIR_EMPTY + k % kPairs));
+      }
+      if (!ok) {  // nothing of this warp's may land after the CTA has ended
+        *abort_flag = 1;
+        for (int s = 0; s < NS; ++s)
+          if (filled & (1u << s)) mbar_wait(bar(Lay::FULL + s), (phases >> s) & 1u, a.err, ERR_WAIT_DRAIN, kDrainLimitNs);
+        if (items_done > 0) mbar_wait(bar(Lay::Q_FULL + g), (items_done - 1) & 1, a.err, ERR_WAIT_DRAIN, kDrainLimitNs);
+      }
+    } else if (warp == 1) {
+      if (lane == 0) {
+        // ---------------- MMA issuer
+        const uint32_t tm = *tmem_slot;
+        bool any = false, ok = true;
+        Place<NS> at;
+        uint32_t tiles_done[2] = {0, 0}, items_done[2] = {0, 0};
+        auto take = [&]() -> bool {
+          return mbar_wait_or_abort(bar(Lay::FULL + at.slot), at.ph, abort_flag, a.err, ERR_WAIT_TMA);
+        };
+        auto give = [&]() {
+          any = true;
+          tc_commit(bar(Lay::EMPTY + at.slot));
+          at.advance(1);
+        };
+        auto issue_s = [&](int g, bool two, bool last) -> bool {  // S_g = Q_g K^T of the item's next tile
+          if (!take()) return false;
+          tc_fence_after();
+          const uint64_t qd = smem_desc_sw128(sb + Lay::Q_OFF + g * Lay::TILE, 16, 1024);
+          const uint64_t kd = smem_desc_sw128(sb + Lay::RING_OFF + at.slot * Lay::TILE, 16, 1024);
+          if (two) {
+#pragma unroll
+            for (int k = 0; k < DH / 16; ++k) {
+              const uint32_t step = ((k >> 2) * kBox + (k & 3) * 32) >> 4;  // of the address field
+              mma_f16(tm + Lay::S_COL(g), desc_add(qd, step), desc_add(kd, step), IDESC_S, k > 0 ? 1u : 0u);
+            }
+          } else {  // one unit: a path of its own, since a choice inside the unrolled one slows every tile
+#pragma unroll 1
+            for (int k = 0; k < DH / 16; ++k) {
+              const uint32_t step = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+              mma_f16(tm + Lay::S_COL(g), desc_add(qd, step), desc_add(kd, step), IDESC_S_HALF, k > 0 ? 1u : 0u);
+            }
+          }
+          tc_commit(bar(Lay::S_FULL + g));
+          if (last) tc_commit(bar(Lay::Q_EMPTY + g));
+          give();
+          return true;
+        };
+        auto issue_pv = [&](int g, bool two, bool fresh) -> bool {  // O_g (+)= P_g V
+          if (!mbar_wait_or_abort(bar(Lay::P_FULL + g), tiles_done[g] & 1, abort_flag, a.err, ERR_WAIT_EPI)) return false;
+          ++tiles_done[g];
+          if (!take()) return false;
+          tc_fence_after();
+          const uint64_t vd = smem_desc_sw128(sb + Lay::RING_OFF + at.slot * Lay::TILE, kBox, 1024);
+          if (two) {
+#pragma unroll
+            for (int k = 0; k < kTile / 16; ++k)
+              mma_f16_ts(tm + Lay::O_COL(g), tm + Lay::S_COL(g) + k * 8, desc_add(vd, k * 2048 >> 4), IDESC_PV,
+                         (!fresh || k > 0) ? 1u : 0u);
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < kUnit / 16; ++k)
+              mma_f16_ts(tm + Lay::O_COL(g), tm + Lay::S_COL(g) + k * 8, desc_add(vd, k * 2048 >> 4), IDESC_PV,
+                         (!fresh || k > 0) ? 1u : 0u);
+          }
+          give();
+          return true;
+        };
+        for (int k = 0; ok; ++k) {
+          const Item* pair = pair_items(k, 1u);
+          if (!pair) { ok = false; break; }
+          const int n0 = pair->tiles, n1 = second(pair)->tiles;
+          if (n0 < 0) break;
+          const int units0 = pair->units, units1 = second(pair)->units;
+          mbar_arrive(bar(Lay::PAIR_EMPTY + k % kPairs));
+          auto first = [&](int g, int units) -> bool {
+            if (units == 0) return true;
+            if (!mbar_wait_or_abort(bar(Lay::Q_FULL + g), items_done[g] & 1, abort_flag, a.err, ERR_WAIT_TMA)) return false;
+            ++items_done[g];
+            return issue_s(g, units > 1, units <= 2);
+          };
+          auto round = [&](int g, int units, int n, int t) -> bool {
+            if (t >= n) return true;
+            if (!issue_pv(g, units - 2 * t > 1, t == 0)) return false;
+            if (t + 1 < n) return issue_s(g, units - 2 * (t + 1) > 1, t + 2 == n);
+            tc_commit(bar(Lay::FIN + g));
+            return true;
+          };
+          ok = first(0, units0) && first(1, units1);
+          const int n = max(n0, n1);
+          for (int t = 0; t < n && ok; ++t) ok = round(0, units0, n0, t) && round(1, units1, n1, t);
+        }
+        if (!ok) {
+          *abort_flag = 1;
+          if (any) {
+            tc_commit(bar(Lay::DRAIN));
+            mbar_wait(bar(Lay::DRAIN), 0, a.err, ERR_WAIT_DRAIN, kDrainLimitNs);
+          }
+        }
+      }
+    } else {
+      // ---------------- the next pair (whole warp)
+      int cta = blockIdx.x;
+      bool ok = true;
+      for (int k = 0; ok && cta >= 0; ++k) {
+        // the place's pair before this one has been let go by all: no CTA is taken over earlier
+        // than when the pair before it is begun, so the last ones go to whoever is free
+        const bool free_ = mbar_wait_or_abort(bar(Lay::PAIR_EMPTY + k % kPairs), ((k / kPairs) & 1) ^ 1, abort_flag, a.err,
+                                              ERR_WAIT_EPI);
+        ok = __all_sync(0xFFFFFFFFu, free_);
+        if (!ok) break;
+        if (k > 0) {
+          if (lane == 0) {
+            fence_proxy_async_smem();  // the response before was read from the same place
+            mbar_arrive_expect_tx(bar(Lay::CANCEL), 16);
+            request_cta(sb + Lay::RESPONSE_OFF, bar(Lay::CANCEL));
+          }
+          __syncwarp();
+          // not given up on an abort: no response may land after the CTA has ended
+          const bool answered = mbar_wait(bar(Lay::CANCEL), (k - 1) & 1, a.err, ERR_WAIT_DRAIN);
+          ok = __all_sync(0xFFFFFFFFu, answered);
+          if (!ok) break;
+          cta = taken_cta(sb + Lay::RESPONSE_OFF);
+          __syncwarp();
+        }
+        Item it0{}, it1{};
+        it0.tiles = -1;
+        if (cta >= 0) {
+          it0 = load_item(p, 2 * cta, lane);
+          it1 = load_item(p, 2 * cta + 1, lane);
         }
         if (lane == 0) {
-          const int nu = min(2, it[g].units - 2 * t);
-          const uint32_t dst = sb0 + Lay::RING_OFF + slot * Lay::TILE;
-          mbar_arrive_expect_tx(full(slot), nu * Lay::NBOX * kUnitBox);
-          for (int u = 0; u < nu; ++u)
-            for (int b = 0; b < Lay::NBOX; ++b)
-              tma_load_3d(dst + b * kBox + u * kUnitBox, tm, full(slot), b * 64, u ? at[g].y : at[g].x, it[g].kvrow);
+          Item* to = reinterpret_cast<Item*>(smem + Lay::ITEM_OFF + (k % kPairs) * 2 * kItemBytes);
+          *to = it0;
+          *const_cast<Item*>(second(to)) = it1;
+          mbar_arrive(bar(Lay::PAIR_FULL + k % kPairs));
         }
-        ++used;
-        if (++slot == NS) {
-          slot = 0;
-          ph ^= 1u;
-        }
-        return true;
-      };
-      auto load_k = [&](int g, int t) -> bool {
-        at[g] = walk[g].tile(it[g], t, a.block_k, a.nkb, none, lane);
-        return load(&tmk, g, t);
-      };
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        walk[g].start(it[g], per_tile, lane);
-        if (it[g].tiles > 0) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(q_full(g), Lay::TILE);
-            for (int b = 0; b < Lay::NBOX; ++b)
-              tma_load_3d(sb0 + Lay::Q_OFF + g * Lay::TILE + b * kBox, &tmq, q_full(g), b * 64,
-                          it[g].qb * kSparseQueries, it[g].bh);
-          }
-          ok = ok && load_k(g, 0);
-        }
+        __syncwarp();
       }
-      const int n = max(it[0].tiles, it[1].tiles);
-      for (int t = 0; t < n && ok; ++t) {
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (ok && t < it[g].tiles) ok = load(&tmv, g, t);
-          if (ok && t + 1 < it[g].tiles) ok = load_k(g, t + 1);
-        }
-      }
-      // the loads still in flight land before the CTA may end; on the regular path every slot in
-      // use has also been consumed
       if (!ok) *abort_flag = 1;
-      const int live = min(used, NS);
-      for (int k = 0; k < live; ++k) {
-        if (--slot < 0) {
-          slot = NS - 1;
-          ph ^= 1u;
-        }
-        if (ok) mbar_wait(empty(slot), ph, a.err, ERR_WAIT_MMA);
-        else mbar_wait(full(slot), ph, a.err, ERR_WAIT_DRAIN, kDrainLimitNs);
-      }
-      if (!ok)
-        for (int g = 0; g < 2; ++g)
-          if (it[g].tiles > 0) mbar_wait(q_full(g), 0, a.err, ERR_WAIT_DRAIN, kDrainLimitNs);
-    } else if (warp == 1 && lane == 0) {
-      // ---------------- MMA issuer
-      int units[2], tiles[2];
-      for (int g = 0; g < 2; ++g) {
-        const Item it = load_item(p, 2 * blockIdx.x + g);
-        units[g] = it.units;
-        tiles[g] = it.tiles;
-      }
-      bool any = false;
-      int slot = 0;
-      uint32_t ph = 0;
-      auto take = [&]() -> bool { return mbar_wait_or_abort(full(slot), ph, abort_flag, a.err, ERR_WAIT_TMA); };
-      auto give = [&]() {
-        tc_commit(empty(slot));
-        if (++slot == NS) {
-          slot = 0;
-          ph ^= 1u;
-        }
-      };
-      auto issue_s = [&](int g, int t) -> bool {  // S_g(t) = Q_g K_t^T
-        if (!take()) return false;
-        tc_fence_after();
-        const uint32_t q_addr = sb0 + Lay::Q_OFF + g * Lay::TILE;
-        const uint32_t k_addr = sb0 + Lay::RING_OFF + slot * Lay::TILE;
-        const uint32_t idesc = units[g] - 2 * t > 1 ? IDESC_S : IDESC_S_HALF;
-#pragma unroll
-        for (int k = 0; k < DH / 16; ++k) {
-          const uint64_t ad = smem_desc_sw128(q_addr + (k >> 2) * kBox + (k & 3) * 32, 16, 1024);
-          const uint64_t bd = smem_desc_sw128(k_addr + (k >> 2) * kBox + (k & 3) * 32, 16, 1024);
-          mma_f16(tmem + Lay::S_COL(g), ad, bd, idesc, k > 0 ? 1u : 0u);
-        }
-        any = true;
-        tc_commit(s_full(g));
-        give();
-        return true;
-      };
-      auto issue_pv = [&](int g, int t) -> bool {  // O_g += P_g(t) V_t
-        if (!mbar_wait_or_abort(p_full(g), t & 1, abort_flag, a.err, ERR_WAIT_EPI)) return false;
-        if (!take()) return false;
-        tc_fence_after();
-        const uint32_t v_addr = sb0 + Lay::RING_OFF + slot * Lay::TILE;
-        const int steps = units[g] - 2 * t > 1 ? kTile / 16 : kUnit / 16;
-#pragma unroll
-        for (int k = 0; k < kTile / 16; ++k) {
-          if (k >= steps) break;
-          const uint64_t bd = smem_desc_sw128(v_addr + k * 2048, kBox, 1024);
-          mma_f16_ts(tmem + Lay::O_COL(g), tmem + Lay::S_COL(g) + k * 8, bd, IDESC_PV, (t > 0 || k > 0) ? 1u : 0u);
-        }
-        any = true;
-        give();
-        return true;
-      };
-      bool ok = true;
-      for (int g = 0; g < 2 && ok; ++g)
-        if (tiles[g] > 0) ok = mbar_wait_or_abort(q_full(g), 0, abort_flag, a.err, ERR_WAIT_TMA) && issue_s(g, 0);
-      const int n = max(tiles[0], tiles[1]);
-      for (int t = 0; t < n && ok; ++t)
-        for (int g = 0; g < 2 && ok; ++g) {
-          if (t >= tiles[g]) continue;
-          ok = issue_pv(g, t);
-          if (!ok) break;
-          if (t + 1 < tiles[g]) ok = issue_s(g, t + 1);
-          else tc_commit(fin(g));
-        }
-      if (!ok) {
-        *abort_flag = 1;
-        if (any) {
-          tc_commit(drain);
-          mbar_wait(drain, 0, a.err, ERR_WAIT_DRAIN, kDrainLimitNs);
-        }
-      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -350,137 +512,158 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
-    const uint32_t s_col = tmem + t_lane + Lay::S_COL(g), o_col = tmem + t_lane + Lay::O_COL(g);
-    const int item = 2 * blockIdx.x + g;
-    const Item it = load_item(p, item);
-    const int other = load_item(p, 2 * blockIdx.x + (g ^ 1)).tiles;
-    const int q = it.qb * kSparseQueries + row;
-    const bool live = it.qb * kSparseQueries + quad * 32 < it.qn;  // warp-uniform: a valid row in this warp
+    const uint32_t s_col = *tmem_slot + t_lane + Lay::S_COL(g), o_col = *tmem_slot + t_lane + Lay::O_COL(g);
     const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
-    ListWalk walk;
-    walk.start(it, per_tile, lane);
-    float m_run = kNoMax, l_run = 0.0f;
+    uint32_t tiles_done = 0, items_done = 0;
+    Place<NS> place;  // of the pair's first load
     bool ok = true;
-    for (int t = 0; t < it.tiles; ++t) {
-      const int2 at = walk.tile(it, t, a.block_k, a.nkb, none, lane);
-      const int nv0 = at.x == none ? 0 : min(kUnit, it.kn - at.x);
-      const int nv1 = at.y == none ? 0 : min(kUnit, it.kn - at.y);
-      const bool s_ok = mbar_wait_or_abort(s_full(g), t & 1, abort_flag, a.err, ERR_WAIT_MMA);
-      if (!__all_sync(0xFFFFFFFFu, s_ok)) { ok = false; break; }
-      // V rows behind kv_len (in memory, so TMA does not zero them) are zeroed once V_t has landed. S_g(t) is
-      // complete, so every load up to K_g(t) has been used, among them the one that held V_g(t)'s
-      // slot before (at least five loads earlier): the parity cannot be of an older phase
-      const bool cut0 = nv0 > 0 && nv0 < kUnit && it.kn < a.Lk, cut1 = nv1 > 0 && nv1 < kUnit && it.kn < a.Lk;
-      if (cut0 || cut1) {
-        // place of V_g(t) in the order of loads: the first K tiles, the loads of the rounds
-        // before t, and item 0's loads of this round
-        const int n0 = g ? other : it.tiles, n1 = g ? it.tiles : other;
-        int pos = (n0 > 0) + (n1 > 0) + min(t, n0) + min(t, max(n0 - 1, 0)) + min(t, n1) + min(t, max(n1 - 1, 0));
-        if (g == 1) pos += (t < n0) + (t + 1 < n0);
-        const int slot = pos % NS;
-        const bool v_ok = mbar_wait_or_abort(full(slot), (pos / NS) & 1, abort_flag, a.err, ERR_WAIT_TMA);
-        if (!__all_sync(0xFFFFFFFFu, v_ok)) { ok = false; break; }
-        for (int u = 0; u < 2; ++u) {
-          if (!(u ? cut1 : cut0)) continue;
-          for (int x = (u ? nv1 : nv0) * 8 + row; x < kUnit * 8; x += 128)
-            for (int b = 0; b < Lay::NBOX; ++b)
-              *reinterpret_cast<uint4*>(smem + Lay::RING_OFF + slot * Lay::TILE + b * kBox + u * kUnitBox + x * 16) =
-                  make_uint4(0, 0, 0, 0);
+    for (int k = 0; ok; ++k) {
+      const volatile Item* pair = pair_items(k, 0xFFFFFFFFu);
+      if (!pair) { ok = false; break; }
+      if (pair->tiles < 0) break;
+      const volatile Item* it = g ? second(const_cast<const Item*>(pair)) : pair;
+      const int tiles = it->tiles;
+      const bool live = it->qb * kSparseQueries + quad * 32 < it->qn;  // warp-uniform: a valid row in this warp
+      // valid keys of unit u (counted from the item's first): the entry's block ends at kv_len
+      auto valid_keys = [&](int u) {
+        if (u >= it->units) return 0;
+        const bool wide = a.block_k == kTile;
+        const int v = __ldg(const_cast<const int*>(it->list) + (wide ? it->t0 + (u >> 1) : 2 * it->t0 + u));
+        if ((unsigned)v >= (unsigned)a.nkb) return 0;
+        return min(kUnit, max(0, it->kn - v * a.block_k - (wide ? (u & 1) * kUnit : 0)));
+      };
+      // every tile but a last one of one unit holds 128 valid keys
+      const int whole = it->clean ? it->units / 2 : 0;
+      float m_run = kNoMax, l_run = 0.0f;
+      for (int t = 0; t < tiles; ++t) {
+        int nv0 = kUnit, nv1 = kUnit;
+        if (t >= whole) {
+          nv0 = valid_keys(2 * t);
+          nv1 = valid_keys(2 * t + 1);
         }
-        fence_proxy_async_smem();
-      }
-      if (live) {
-        tc_fence_after();
-        uint32_t sr[kTile];
-#pragma unroll
-        for (int c = 0; c < kTile / 32; ++c)
-          tmem_ld32(s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < kTile / 32; ++c) tmem_reg_fence(*reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-        if (nv0 < kUnit || nv1 < kUnit) {  // warp-uniform
-#pragma unroll
-          for (int i = 0; i < kTile; ++i)
-            if ((i & (kUnit - 1)) >= (i < kUnit ? nv0 : nv1)) sr[i] = __float_as_uint(-INFINITY);
-        }
-        // row max with 8 independent partial maxima; NaN if a score is (then the row's sum is NaN too,
-        // whichever pipe computes that score's exponential)
-        float pm[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) pm[e] = __uint_as_float(sr[e]);
-#pragma unroll
-        for (int i = 8; i < kTile; i += 16)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) pm[e] = max3_nan(pm[e], __uint_as_float(sr[i + e]), __uint_as_float(sr[i + 8 + e]));
-        const float mx = max3_nan(max3_nan(pm[0], pm[1], pm[2]), max3_nan(pm[3], pm[4], pm[5]), max3_nan(pm[6], pm[7], kNoMax));
-        // finite also where every key of the tile is masked, so that exp2(-inf - m) is 0; an infinite
-        // score makes it NaN, as inf - inf does in the formula
-        const float mxs = fmaf(0.0f, mx, mx * p.scale_log2);
-        float alpha = 1.0f;
-        bool rescale = false;
-        if (t == 0) {
-          m_run = mxs;  // O is not there yet
-        } else if (!(mxs <= m_run + 8.0f)) {  // NaN as well
-          alpha = fast_exp2(m_run - mxs);
-          m_run = mxs;
-          rescale = true;
-        }
-        // p = exp2(s * c - m), packed to bf16 pairs in place; sum with 4 packed accumulators
-        const float2 nm2 = make_float2(-m_run, -m_run);
-        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int i = 0; i < kTile; i += 2) {
-          const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), c2, nm2);
-          float2 e;
-          if (kPolyMod > 0 && (i >> 1) % (kPolyMod > 0 ? kPolyMod : 1) == kPolyMod - 1)
-            e = exp2_poly2(x);
-          else
-            e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          acc[(i >> 1) & 3] = __fadd2_rn(acc[(i >> 1) & 3], e);
-          sr[i >> 1] = pack_bf16x2(e.x, e.y);
-        }
-        const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
-        const float2 a03 = __fadd2_rn(a01, a23);
-        l_run = fmaf(l_run, alpha, a03.x + a03.y);
-        // S_g(t) complete => PV_g(t-1) complete: O_g is stable until P_g(t) is published.
-        if (__any_sync(0xFFFFFFFFu, rescale)) {
-#pragma unroll
-          for (int c = 0; c < DH / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(o_col + c * 32, o);
-            tmem_ld_wait();
-            tmem_reg_fence(o);
-#pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
-                                          make_float2(alpha, alpha));
-              o[e] = __float_as_uint(v.x);
-              o[e + 1] = __float_as_uint(v.y);
-            }
-            tmem_st32(o_col + c * 32, o);
+        const bool s_ok =
+            mbar_wait_or_abort(bar(Lay::S_FULL + g), tiles_done & 1, abort_flag, a.err, ERR_WAIT_MMA);
+        if (!__all_sync(0xFFFFFFFFu, s_ok)) { ok = false; break; }
+        ++tiles_done;
+        // V rows behind kv_len (in memory, so TMA does not zero them) are zeroed once V_t has landed. S_g(t) is
+        // complete, so every load up to K_g(t) has been used, among them the one that held V_g(t)'s
+        // slot before (at least five loads earlier): the parity cannot be of an older phase
+        const bool cut0 = nv0 > 0 && nv0 < kUnit, cut1 = nv1 > 0 && nv1 < kUnit;
+        if ((cut0 || cut1) && it->kn < a.Lk) {
+          // place of V_g(t) in the order of loads: the first K tiles, the loads of the rounds
+          // before t, and item 0's loads of this round
+          const int n0 = pair->tiles, n1 = second(const_cast<const Item*>(pair))->tiles;
+          int pos = (n0 > 0) + (n1 > 0) + min(t, n0) + min(t, max(n0 - 1, 0)) + min(t, n1) + min(t, max(n1 - 1, 0));
+          if (g == 1) pos += (t < n0) + (t + 1 < n0);
+          Place<NS> at = place;
+          at.advance_any(pos);
+          const bool v_ok = mbar_wait_or_abort(bar(Lay::FULL + at.slot), at.ph, abort_flag, a.err, ERR_WAIT_TMA);
+          if (!__all_sync(0xFFFFFFFFu, v_ok)) { ok = false; break; }
+          for (int u = 0; u < 2; ++u) {
+            if (!(u ? cut1 : cut0)) continue;
+            for (int x = (u ? nv1 : nv0) * 8 + row; x < kUnit * 8; x += 128)
+              for (int b = 0; b < Lay::NBOX; ++b)
+                *reinterpret_cast<uint4*>(smem + Lay::RING_OFF + at.slot * Lay::TILE + b * kBox + u * kUnitBox + x * 16) =
+                    make_uint4(0, 0, 0, 0);
           }
+          fence_proxy_async_smem();
         }
-        // P_g(t) over the first 64 columns of S_g: column c holds keys 2c (low half) and 2c+1.
-        tmem_st32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-        tmem_st32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-        tmem_st_wait();
-        tc_fence_before();
+        if (live) {
+          tc_fence_after();
+          uint32_t sr[kTile];
+  #pragma unroll
+          for (int c = 0; c < kTile / 32; ++c)
+            tmem_ld32(s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          tmem_ld_wait();
+  #pragma unroll
+          for (int c = 0; c < kTile / 32; ++c) tmem_reg_fence(*reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          if (nv0 < kUnit || nv1 < kUnit) {  // warp-uniform
+  #pragma unroll
+            for (int i = 0; i < kTile; ++i)
+              if ((i & (kUnit - 1)) >= (i < kUnit ? nv0 : nv1)) sr[i] = __float_as_uint(-INFINITY);
+          }
+          // row max with 8 independent partial maxima; NaN if a score is (then the row's sum is NaN too,
+          // whichever pipe computes that score's exponential)
+          float pm[8];
+  #pragma unroll
+          for (int e = 0; e < 8; ++e) pm[e] = __uint_as_float(sr[e]);
+  #pragma unroll
+          for (int i = 8; i < kTile; i += 16)
+  #pragma unroll
+            for (int e = 0; e < 8; ++e) pm[e] = max3_nan(pm[e], __uint_as_float(sr[i + e]), __uint_as_float(sr[i + 8 + e]));
+          const float mx = max3_nan(max3_nan(pm[0], pm[1], pm[2]), max3_nan(pm[3], pm[4], pm[5]), max3_nan(pm[6], pm[7], kNoMax));
+          // finite also where every key of the tile is masked, so that exp2(-inf - m) is 0; an infinite
+          // score makes it NaN, as inf - inf does in the formula
+          const float mxs = fmaf(0.0f, mx, mx * p.scale_log2);
+          float alpha = 1.0f;
+          bool rescale = false;
+          if (t == 0) {
+            m_run = mxs;  // O is not there yet
+          } else if (!(mxs <= m_run + 8.0f)) {  // NaN as well
+            alpha = fast_exp2(m_run - mxs);
+            m_run = mxs;
+            rescale = true;
+          }
+          // p = exp2(s * c - m), packed to bf16 pairs in place; sum with 4 packed accumulators
+          const float2 nm2 = make_float2(-m_run, -m_run);
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  #pragma unroll
+          for (int i = 0; i < kTile; i += 2) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), c2, nm2);
+            float2 e;
+            if (kPolyMod > 0 && (i >> 1) % (kPolyMod > 0 ? kPolyMod : 1) == kPolyMod - 1)
+              e = exp2_poly2(x);
+            else
+              e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            acc[(i >> 1) & 3] = __fadd2_rn(acc[(i >> 1) & 3], e);
+            sr[i >> 1] = pack_bf16x2(e.x, e.y);
+          }
+          const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+          const float2 a03 = __fadd2_rn(a01, a23);
+          l_run = fmaf(l_run, alpha, a03.x + a03.y);
+          // S_g(t) complete => PV_g(t-1) complete: O_g is stable until P_g(t) is published.
+          if (__any_sync(0xFFFFFFFFu, rescale)) {
+  #pragma unroll
+            for (int c = 0; c < DH / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(o_col + c * 32, o);
+              tmem_ld_wait();
+              tmem_reg_fence(o);
+  #pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
+                                            make_float2(alpha, alpha));
+                o[e] = __float_as_uint(v.x);
+                o[e + 1] = __float_as_uint(v.y);
+              }
+              tmem_st32(o_col + c * 32, o);
+            }
+          }
+          // P_g(t) over the first 64 columns of S_g: column c holds keys 2c (low half) and 2c+1.
+          tmem_st32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+          tmem_st32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+          tmem_st_wait();
+        }
+        tc_fence_before();  // P is there, and O of the item before has been read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Lay::P_FULL + g));
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full(g));
-    }
-    const bool f_ok =
-        ok && (it.tiles == 0 || mbar_wait_or_abort(fin(g), 0, abort_flag, a.err, ERR_WAIT_MMA));
-    if (__all_sync(0xFFFFFFFFu, f_ok)) {
+      if (!ok) break;
+      if (tiles > 0) {
+        const bool f_ok = mbar_wait_or_abort(bar(Lay::FIN + g), items_done & 1, abort_flag, a.err, ERR_WAIT_MMA);
+        if (!__all_sync(0xFFFFFFFFu, f_ok)) { ok = false; break; }
+        ++items_done;
+      }
       tc_fence_after();
       if (live) {  // warp-uniform
-        const bool mine = q < it.qn;
+        const int item = (it->bh * a.nqb + it->qb) * p.nsplit + it->t0 / p.split_tiles;
+        const int q = it->qb * kSparseQueries + row;
+        const bool mine = q < it->qn;
         const bool empty_row = l_run == 0.0f;  // no valid key: O was never written, or only with zeros
-        const int b = it.bh / a.n_heads, h = it.bh - b * a.n_heads;
+        const int b = it->bh / a.n_heads, h = it->bh - b * a.n_heads;
         const int dm = a.n_heads * DH;
         const long long o_at = ((long long)b * a.Lq + q) * dm + h * DH;
         const long long part_at = ((long long)item * kSparseQueries + row) * DH;
-        const long long part_n = (long long)p.rows * p.nsplit * kSparseQueries;
         const float inv_l = 1.0f / l_run;
         const float2 il2 = make_float2(inv_l, inv_l);
         float amax = 0.0f;
@@ -491,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           tmem_reg_fence(o);
           if (p.nsplit > 1) {
-            if (mine && !empty_row && H3B_IDX_OK(part_at + c * 32 + 31, part_n * DH, a.err)) {
+            if (mine && !empty_row && H3B_IDX_OK(part_at + c * 32 + 31, (long long)p.rows * p.nsplit * kSparseQueries * DH, a.err)) {
               uint4* d4 = reinterpret_cast<uint4*>(p.part_o + part_at + c * 32);
 #pragma unroll
               for (int e = 0; e < 8; ++e) d4[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -513,22 +696,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (mine) {
           if (p.nsplit > 1) {
-            if (H3B_IDX_OK((long long)item * kSparseQueries + row, part_n, a.err))
+            if (H3B_IDX_OK((long long)item * kSparseQueries + row, (long long)p.rows * p.nsplit * kSparseQueries, a.err))
               p.part_ml[(size_t)item * kSparseQueries + row] = make_float2(m_run, l_run);
           } else if (a.absmax && H3B_IDX_OK((long long)b * a.Lq + q, (long long)a.B * a.Lq, a.err)) {
             atomicMax(reinterpret_cast<unsigned*>(a.absmax) + (size_t)b * a.Lq + q, __float_as_uint(amax));
           }
         }
       }
-    } else {
-      *abort_flag = 1;
+      place.advance_any(2 * (max(pair->tiles, 0) + second(const_cast<const Item*>(pair))->tiles));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Lay::PAIR_EMPTY + k % kPairs));
     }
+    if (!ok) *abort_flag = 1;
   }
   __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc(*tmem_slot, kTmemCols);
   }
 }
 
