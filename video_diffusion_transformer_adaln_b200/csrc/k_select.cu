@@ -3,31 +3,110 @@
 // and the topk best key blocks of each query block, ties to the lower index.
 // The means and the scores are in 64 bits: a list is decided by comparisons, so
 // two scores closer than their rounding errors would be listed by accident.
+//
+// Two kernels. The means read q and k once, 16 bytes a lane, and are bound by
+// HBM. The scores are a product in 64 bits, [16 query blocks] x [all key blocks]
+// per CTA, on the FP64 pipe (64 a cycle and SM), whose key means come from L2
+// transposed, two keys a thread; the topk of a row is found by a warp, by
+// bisection over the bits of the scores mapped to unsigned integers.
 #include "h3b_common.cuh"
 #include "h3b_internal.h"
 
 namespace h3b {
 namespace {
 
-constexpr int kMaxKeyBlocks = 4096;
-
 __device__ __forceinline__ int clamp_len(const int* lens, int b, int L) {
-  return lens ? min(max(lens[b], 0), L) : L;
+  return lens ? min(max(__ldg(lens + b), 0), L) : L;
 }
 
-// means[row][block][lane]: a block per (row = batch item x head, block), a thread per lane.
-__global__ void __launch_bounds__(128) block_means_kernel(const __nv_bfloat16* __restrict__ x, const int* lens, int heads,
-                                                          int L, int DH, int size, int n_blocks, double* means,
-                                                          long long n_means, unsigned* err) {
+constexpr int kMeanThreads = 256;
+
+// Where the means lie in the workspace: q [row][query block][lane]; k transposed, [row][lane][key block],
+// rows of an even number of key blocks.
+struct Means {
+  double *q, *k;
+  long long nq, nk;  // elements
+  int nkb_even;
+};
+
+Means means_of(void* ws, int B, int n_heads, int n_kv_heads, int DH, int nqb, int nkb) {
+  Means m;
+  m.nkb_even = (nkb + 1) & ~1;
+  m.nq = (long long)B * n_heads * nqb * DH;
+  m.nk = (long long)B * n_kv_heads * m.nkb_even * DH;
+  m.q = static_cast<double*>(ws);
+  m.k = m.q + m.nq;
+  return m;
+}
+
+// A CTA per block of rows: DH / 8 lanes per row, ITERS rows per thread, all of them loaded before any is
+// used. Rows are added in pairs in 32 bits (two bf16 values of like size add exactly) and the pairs in
+// 64, which halves the work of the FP64 pipe: its conversions would take as long as the loads.
+template <int DH, int ITERS>
+__device__ __forceinline__ void block_mean(const __nv_bfloat16* p, int n, double* out, long long out_stride,
+                                           double (*part)[DH]) {
+  constexpr int LPR = DH / 8, RPI = kMeanThreads / LPR, ROWS_PER_WARP = 32 / LPR;
+  const int sub = threadIdx.x % LPR, r0 = threadIdx.x / LPR, warp = threadIdx.x >> 5;
+  const uint4* src = reinterpret_cast<const uint4*>(p) + sub;
+  uint4 v[ITERS];
+#pragma unroll
+  for (int i = 0; i < ITERS; ++i) {
+    const int r = r0 + i * RPI;
+    v[i] = r < n ? __ldg(src + (size_t)r * LPR) : make_uint4(0, 0, 0, 0);
+  }
+  double s[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s[e] = 0.0;
+#pragma unroll
+  for (int i = 0; i < ITERS; i += 2) {
+    const uint32_t a[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    const uint32_t b[4] = {v[i + 1].x, v[i + 1].y, v[i + 1].z, v[i + 1].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s[2 * e] += (double)(bf16_lo(a[e]) + bf16_lo(b[e]));
+      s[2 * e + 1] += (double)(bf16_hi(a[e]) + bf16_hi(b[e]));
+    }
+  }
+#pragma unroll
+  for (int o = LPR; o < 32; o <<= 1)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e] += __shfl_xor_sync(0xFFFFFFFFu, s[e], o);
+  static_assert(ROWS_PER_WARP * LPR == 32, "a warp holds whole rows");
+  if ((threadIdx.x & 31) < LPR) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[warp][sub * 8 + e] = s[e];
+  }
+  __syncthreads();
+  if (threadIdx.x < DH) {
+    double t = 0.0;
+#pragma unroll
+    for (int w = 0; w < kMeanThreads / 32; ++w) t += part[w][threadIdx.x];
+    if (out) out[threadIdx.x * out_stride] = n > 0 ? t / n : 0.0;
+  }
+}
+
+template <int DH, int BK>
+__global__ void __launch_bounds__(kMeanThreads) block_means_kernel(const SelectArgs a, const Means m) {
   griddep_wait();
   griddep_launch_dependents();
-  const int blk = blockIdx.x, row = blockIdx.y;
-  const int n = min(clamp_len(lens, row / heads, L) - blk * size, size);
-  const __nv_bfloat16* p = x + ((size_t)row * L + (size_t)blk * size) * DH + threadIdx.x;
-  double s = 0.0;
-  for (int i = 0; i < n; ++i) s += (double)__bfloat162float(p[(size_t)i * DH]);
-  const long long at = ((long long)row * n_blocks + blk) * DH + threadIdx.x;
-  if (H3B_IDX_OK(at, n_means, err)) means[at] = n > 0 ? s / n : 0.0;
+  __shared__ double part[kMeanThreads / 32][DH];
+  constexpr int RPI = kMeanThreads / (DH / 8);
+  const int nq = a.B * a.n_heads * a.nqb;
+  if ((int)blockIdx.x < nq) {
+    const int row = blockIdx.x / a.nqb, blk = blockIdx.x - row * a.nqb;
+    const int n = min(max(clamp_len(a.q_lens, row / a.n_heads, a.Lq) - blk * kSparseQueries, 0), kSparseQueries);
+    const long long at = (long long)blockIdx.x * DH;
+    block_mean<DH, kSparseQueries / RPI>(static_cast<const __nv_bfloat16*>(a.q) + ((size_t)row * a.Lq + (size_t)blk * kSparseQueries) * DH,
+                                         n, H3B_IDX_OK(at + DH - 1, m.nq, a.err) ? m.q + at : nullptr, 1, part);
+  } else {
+    const int id = blockIdx.x - nq;
+    const int row = id / a.nkb, blk = id - row * a.nkb;
+    const int n = min(max(clamp_len(a.kv_lens, row / a.n_kv_heads, a.Lk) - blk * BK, 0), BK);
+    const long long at = (long long)row * DH * m.nkb_even + blk;
+    block_mean<DH, BK / RPI>(static_cast<const __nv_bfloat16*>(a.k) + ((size_t)row * a.Lk + (size_t)blk * BK) * DH, n,
+                             H3B_IDX_OK(at + (long long)(DH - 1) * m.nkb_even, m.nk, a.err) ? m.k + at : nullptr,
+                             m.nkb_even, part);
+  }
 }
 
 // The order of the scores as unsigned integers: higher is better, -0 equals +0, NaN is last.
@@ -38,82 +117,140 @@ __device__ __forceinline__ unsigned long long order_key(double s) {
 }
 constexpr unsigned long long kKeyKeep = ~0ull;
 
-// A block per (query block, batch item x head): scores of all key blocks, then each block's rank.
-__global__ void __launch_bounds__(256) select_kernel(const SelectArgs a, const double* qm, const double* km) {
+// A CTA per QR query blocks of one head.
+template <int DH, int QR>
+__global__ void __launch_bounds__(256) select_kernel(const SelectArgs a, const Means m) {
   griddep_wait();
   griddep_launch_dependents();
-  extern __shared__ unsigned long long keys[];  // [nkb]
-  __shared__ double qs[128];
-  __shared__ int warp_n[8];
-  const int i = blockIdx.x, row = blockIdx.y, DH = a.head_dim;
+  extern __shared__ double2 smem_select[];
+  double* qs = reinterpret_cast<double*>(smem_select);                                      // [DH][QR]
+  unsigned long long* keys = reinterpret_cast<unsigned long long*>(qs + DH * QR);  // [QR][nkb_even]
+  const int i0 = blockIdx.x * QR, row = blockIdx.y;
   const int b = row / a.n_heads, h = row - b * a.n_heads;
   const int kvrow = b * a.n_kv_heads + h / (a.n_heads / a.n_kv_heads);
   const int qn = clamp_len(a.q_lens, b, a.Lq), kn = clamp_len(a.kv_lens, b, a.Lk);
-  const int cand = i * kSparseQueries < qn ? (kn + a.block_k - 1) / a.block_k : 0;
-  const int want = min(cand, a.topk);
-  if (threadIdx.x < DH) qs[threadIdx.x] = qm[((size_t)row * a.nqb + i) * DH + threadIdx.x];
-  __syncthreads();
-  const int lo = i * kSparseQueries / a.block_k - a.keep_local + 1;
-  const int hi = (i * kSparseQueries + kSparseQueries - 1) / a.block_k + a.keep_local - 1;
-  for (int j = threadIdx.x; j < cand; j += blockDim.x) {
-    const double* kk = km + ((size_t)kvrow * a.nkb + j) * DH;
-    double s = 0.0;
-    for (int e = 0; e < DH; ++e) s = fma(qs[e], kk[e], s);
-    const bool keep = j < a.keep_first || (a.keep_local > 0 && j >= lo && j <= hi);
-    keys[j] = keep ? kKeyKeep : order_key(s);
+  const int cand = (kn + a.block_k - 1) / a.block_k;  // key blocks that hold a valid key
+  const int nke = m.nkb_even;
+  for (int x = threadIdx.x; x < DH * QR; x += blockDim.x) {
+    const int i = x / DH, e = x - i * DH;
+    const long long at = ((long long)row * a.nqb + i0 + i) * DH + e;
+    qs[e * QR + i] = i0 + i < a.nqb && H3B_IDX_OK(at, m.nq, a.err) ? m.q[at] : 0.0;
   }
   __syncthreads();
-  const long long list = (long long)row * a.nqb + i;
-  int* out = a.blocks + list * a.topk;
-  int done = 0;
-  for (int j0 = 0; j0 < cand; j0 += blockDim.x) {
-    const int j = j0 + threadIdx.x;
-    bool take = false;
-    if (j < cand) {
-      const unsigned long long mine = keys[j];
-      int rank = 0;
-      for (int o = 0; o < cand; ++o) rank += keys[o] > mine || (keys[o] == mine && o < j);
-      take = rank < want;
+  const double* km = m.k + (size_t)kvrow * DH * nke;
+  for (int j = 2 * threadIdx.x; j < cand; j += 2 * blockDim.x) {  // keys j, j + 1 of this thread
+    double s0[QR], s1[QR];
+#pragma unroll
+    for (int i = 0; i < QR; ++i) s0[i] = s1[i] = 0.0;
+    const double* kj = km + j;
+#pragma unroll 1
+    for (int e0 = 0; e0 < DH; e0 += 8) {
+      double2 kk[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) kk[e] = __ldg(reinterpret_cast<const double2*>(kj + (size_t)(e0 + e) * nke));
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+#pragma unroll
+        for (int i = 0; i < QR; i += 2) {
+          const double2 q2 = *reinterpret_cast<const double2*>(qs + (e0 + e) * QR + i);
+          s0[i] = fma(q2.x, kk[e].x, s0[i]);
+          s1[i] = fma(q2.x, kk[e].y, s1[i]);
+          s0[i + 1] = fma(q2.y, kk[e].x, s0[i + 1]);
+          s1[i + 1] = fma(q2.y, kk[e].y, s1[i + 1]);
+        }
     }
-    const unsigned m = __ballot_sync(0xFFFFFFFFu, take);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) warp_n[warp] = __popc(m);
-    __syncthreads();
-    int at = done + __popc(m & ((1u << lane) - 1u));
-    for (int w = 0; w < 8; ++w) {
-      if (w < warp) at += warp_n[w];
-      done += warp_n[w];
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {
+      const int lo = (i0 + i) * kSparseQueries / a.block_k - a.keep_local + 1;
+      const int hi = ((i0 + i) * kSparseQueries + kSparseQueries - 1) / a.block_k + a.keep_local - 1;
+      const bool k0 = j < a.keep_first || (a.keep_local > 0 && j >= lo && j <= hi);
+      const bool k1 = j + 1 < a.keep_first || (a.keep_local > 0 && j + 1 >= lo && j + 1 <= hi);
+      keys[i * nke + j] = k0 ? kKeyKeep : order_key(s0[i]);
+      keys[i * nke + j + 1] = k1 ? kKeyKeep : order_key(s1[i]);
     }
-    if (take && H3B_IDX_OK(at, want, a.err)) out[at] = j;
-    __syncthreads();
   }
-  for (int t = want + threadIdx.x; t < a.topk; t += blockDim.x) out[t] = -1;
-  if (threadIdx.x == 0) a.counts[list] = want;
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = warp; i < QR && i0 + i < a.nqb; i += blockDim.x >> 5) {
+    const int n = (i0 + i) * kSparseQueries < qn ? cand : 0;
+    const int want = min(n, a.topk);
+    const unsigned long long* key = keys + i * nke;
+    // the largest T with at least `want` keys >= T, bit by bit; done early when exactly `want` are
+    unsigned long long T = 0;
+    int above = n;  // keys >= T
+    for (int bit = 63; bit >= 0 && above > want; --bit) {
+      const unsigned long long c = T | (1ull << bit);
+      int cnt = 0;
+      for (int j = lane; j < n; j += 32) cnt += key[j] >= c;
+      cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
+      if (cnt >= want) {
+        T = c;
+        above = cnt;
+      }
+    }
+    // above > want: the keys equal to T are more than needed; the lowest of them are listed
+    int ties = above;
+    if (above > want) {
+      int more = 0;
+      for (int j = lane; j < n; j += 32) more += key[j] > T;
+      ties = want - __reduce_add_sync(0xFFFFFFFFu, more);
+    }
+    const long long list = (long long)row * a.nqb + i0 + i;
+    int* out = a.blocks + list * a.topk;
+    int at = 0, seen = 0;  // listed, and equal to T, so far
+    for (int j0 = 0; j0 < n; j0 += 32) {
+      const int j = j0 + lane;
+      const unsigned long long mine = j < n ? key[j] : 0ull;
+      const bool equal = j < n && mine == T;
+      const unsigned below = (1u << lane) - 1u;
+      const unsigned eq = __ballot_sync(0xFFFFFFFFu, equal);
+      const bool take = j < n && (mine > T || (equal && seen + __popc(eq & below) < ties));
+      const unsigned tk = __ballot_sync(0xFFFFFFFFu, take);
+      const int to = at + __popc(tk & below);
+      if (take && H3B_IDX_OK(to, want, a.err)) out[to] = j;
+      at += __popc(tk);
+      seen += __popc(eq);
+    }
+    for (int t = want + lane; t < a.topk; t += 32) out[t] = -1;
+    if (lane == 0) a.counts[list] = want;
+  }
+}
+
+template <int DH, int QR>
+cudaError_t launch_select(const SelectArgs& a, const Means& m, cudaStream_t st) {
+  const size_t smem = sizeof(double) * ((size_t)DH * QR + (size_t)QR * m.nkb_even);
+  auto k = select_kernel<DH, QR>;
+  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int warps = min(max((m.nkb_even / 2 + 31) / 32, 4), 8);
+  return launch_pdl(k, dim3((a.nqb + QR - 1) / QR, a.B * a.n_heads), dim3(32 * warps), smem, st, a, m);
+}
+
+template <int DH>
+cudaError_t launch(const SelectArgs& a, int sms, cudaStream_t st) {
+  const Means m = means_of(a.ws, a.B, a.n_heads, a.n_kv_heads, DH, a.nqb, a.nkb);
+  const long long blocks = (long long)a.B * a.n_heads * a.nqb + (long long)a.B * a.n_kv_heads * a.nkb;
+  const dim3 grid((unsigned)blocks);
+  const cudaError_t e =
+      a.block_k == 64 ? launch_pdl(block_means_kernel<DH, 64>, grid, dim3(kMeanThreads), 0, st, a, m)
+                      : launch_pdl(block_means_kernel<DH, 128>, grid, dim3(kMeanThreads), 0, st, a, m);
+  if (e != cudaSuccess) return e;
+  // 16 query blocks a CTA read each key mean once for 16 products; fewer where that leaves
+  // processors without work, or where 16 rows of scores do not fit the shared memory
+  const long long ctas16 = (long long)a.B * a.n_heads * ((a.nqb + 15) / 16);
+  if (ctas16 >= sms && m.nkb_even <= 1280) return launch_select<DH, 16>(a, m, st);
+  return launch_select<DH, 4>(a, m, st);
 }
 
 }  // namespace
 
 size_t select_ws_bytes(int B, int n_heads, int n_kv_heads, int head_dim, int nqb, int nkb) {
-  return sizeof(double) * (size_t)head_dim * B * ((size_t)n_heads * nqb + (size_t)n_kv_heads * nkb);
+  const Means m = means_of(nullptr, B, n_heads, n_kv_heads, head_dim, nqb, nkb);
+  return sizeof(double) * (size_t)(m.nq + m.nk);
 }
 
 cudaError_t launch_select_blocks(const SelectArgs& a, int sms, cudaStream_t st) {
-  (void)sms;
-  double* qm = static_cast<double*>(a.ws);
-  const long long nq = (long long)a.B * a.n_heads * a.nqb * a.head_dim;
-  const long long nk = (long long)a.B * a.n_kv_heads * a.nkb * a.head_dim;
-  double* km = qm + nq;
-  cudaError_t e = launch_pdl(block_means_kernel, dim3(a.nqb, a.B * a.n_heads), dim3(a.head_dim), 0, st,
-                             static_cast<const __nv_bfloat16*>(a.q), a.q_lens, a.n_heads, a.Lq, a.head_dim,
-                             kSparseQueries, a.nqb, qm, nq, a.err);
-  if (e != cudaSuccess) return e;
-  e = launch_pdl(block_means_kernel, dim3(a.nkb, a.B * a.n_kv_heads), dim3(a.head_dim), 0, st,
-                 static_cast<const __nv_bfloat16*>(a.k), a.kv_lens, a.n_kv_heads, a.Lk, a.head_dim, a.block_k, a.nkb,
-                 km, nk, a.err);
-  if (e != cudaSuccess) return e;
-  static_assert(kMaxKeyBlocks * 8 <= 48 * 1024, "the keys fit the default shared memory");
-  return launch_pdl(select_kernel, dim3(a.nqb, a.B * a.n_heads), dim3(256), (size_t)a.nkb * 8, st, a,
-                    (const double*)qm, (const double*)km);
+  return a.head_dim == 128 ? launch<128>(a, sms, st) : launch<64>(a, sms, st);
 }
 
 }  // namespace h3b
