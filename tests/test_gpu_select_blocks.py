@@ -143,3 +143,10 @@ def test_workspace_size_is_enough():
     counts = torch.empty((2, 2, d.nqb), dtype=torch.int32, device="cuda")
     h3b.h3b_select_blocks(d, q, k, None, None, blocks, counts, buf[:need])
     assert (buf[need:] == 0xA5).all()
+
+
+def test_many_key_blocks():
+    """More key blocks than 16 rows of scores fit in shared memory."""
+    require_gpu()
+    check(field(1, 1, 700, 64, 18), field(1, 1, 64 * 1537, 64, 19), 64, 100, local=1)
+    check(field(1, 2, 130, 128, 20), field(1, 1, 64 * 1536, 128, 21), 64, 9)

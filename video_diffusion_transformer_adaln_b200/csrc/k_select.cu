@@ -6,9 +6,9 @@
 //
 // Two kernels. The means read q and k once, 16 bytes a lane, and are bound by
 // HBM. The scores are a product in 64 bits, [16 query blocks] x [all key blocks]
-// per CTA, on the FP64 pipe (64 a cycle and SM), whose key means come from L2
-// transposed, two keys a thread; the topk of a row is found by a warp, by
-// bisection over the bits of the scores mapped to unsigned integers.
+// per CTA, on the FP64 matrix instruction (16 x 8 x 16), whose key means come
+// from L2; the topk of a row is found by a warp, by bisection over the bits of
+// the scores mapped to unsigned integers.
 #include "h3b_common.cuh"
 #include "h3b_internal.h"
 
@@ -21,19 +21,16 @@ __device__ __forceinline__ int clamp_len(const int* lens, int b, int L) {
 
 constexpr int kMeanThreads = 256;
 
-// Where the means lie in the workspace: q [row][query block][lane]; k transposed, [row][lane][key block],
-// rows of an even number of key blocks.
+// Where the means lie in the workspace: [row = batch item x head][block][lane], q before k.
 struct Means {
   double *q, *k;
   long long nq, nk;  // elements
-  int nkb_even;
 };
 
 Means means_of(void* ws, int B, int n_heads, int n_kv_heads, int DH, int nqb, int nkb) {
   Means m;
-  m.nkb_even = (nkb + 1) & ~1;
   m.nq = (long long)B * n_heads * nqb * DH;
-  m.nk = (long long)B * n_kv_heads * m.nkb_even * DH;
+  m.nk = (long long)B * n_kv_heads * nkb * DH;
   m.q = static_cast<double*>(ws);
   m.k = m.q + m.nq;
   return m;
@@ -45,7 +42,7 @@ Means means_of(void* ws, int B, int n_heads, int n_kv_heads, int DH, int nqb, in
 constexpr int kBatch = 8;  // loads per lane and batch
 
 template <int DH>
-__device__ __forceinline__ void block_mean(const __nv_bfloat16* p, int n, int lane, double* out, long long out_stride) {
+__device__ __forceinline__ void block_mean(const __nv_bfloat16* p, int n, int lane, double* out) {
   constexpr int LPR = DH / 8, RPI = 32 / LPR;
   const int sub = lane % LPR, r0 = lane / LPR;
   const uint4* src = reinterpret_cast<const uint4*>(p) + sub;
@@ -86,8 +83,9 @@ __device__ __forceinline__ void block_mean(const __nv_bfloat16* p, int n, int la
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e] += __shfl_xor_sync(0xFFFFFFFFu, s[e], o);
   if (lane < LPR && out) {
+    double2* to = reinterpret_cast<double2*>(out + sub * 8);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) out[(sub * 8 + e) * out_stride] = n > 0 ? s[e] / n : 0.0;
+    for (int e = 0; e < 4; ++e) to[e] = n > 0 ? make_double2(s[2 * e] / n, s[2 * e + 1] / n) : make_double2(0.0, 0.0);
   }
 }
 
@@ -102,13 +100,13 @@ __global__ void __launch_bounds__(kMeanThreads) block_means_kernel(const SelectA
     const int n = min(max(clamp_len(a.q_lens, row / a.n_heads, a.Lq) - blk * kSparseQueries, 0), kSparseQueries);
     const long long at = (long long)id * DH;
     block_mean<DH>(static_cast<const __nv_bfloat16*>(a.q) + ((size_t)row * a.Lq + (size_t)blk * kSparseQueries) * DH, n, lane,
-                   H3B_IDX_OK(at + DH - 1, m.nq, a.err) ? m.q + at : nullptr, 1);
+                   H3B_IDX_OK(at + DH - 1, m.nq, a.err) ? m.q + at : nullptr);
   } else if (id - nq < nk) {
     const int row = (id - nq) / a.nkb, blk = id - nq - row * a.nkb;
     const int n = min(max(clamp_len(a.kv_lens, row / a.n_kv_heads, a.Lk) - blk * a.block_k, 0), a.block_k);
-    const long long at = (long long)row * DH * m.nkb_even + blk;
+    const long long at = (long long)(id - nq) * DH;
     block_mean<DH>(static_cast<const __nv_bfloat16*>(a.k) + ((size_t)row * a.Lk + (size_t)blk * a.block_k) * DH, n, lane,
-                   H3B_IDX_OK(at + (long long)(DH - 1) * m.nkb_even, m.nk, a.err) ? m.k + at : nullptr, m.nkb_even);
+                   H3B_IDX_OK(at + DH - 1, m.nk, a.err) ? m.k + at : nullptr);
   }
 }
 
@@ -120,83 +118,76 @@ __device__ __forceinline__ unsigned long long order_key(double s) {
 }
 constexpr unsigned long long kKeyKeep = ~0ull;
 
-// A CTA per QR query blocks of one head. Its warps cover `tiles` times 64 keys; with few keys, `parts`
-// warps share a tile's sums over the lanes of the head, and their parts are added in order.
+// D (16 x 8) += A (16 x 16) B (16 x 8) in 64 bits. Lane = 4 g + t holds A[g][.], A[g + 8][.] (a even, odd),
+// B[.][g] and D[g][2t], D[g][2t + 1], D[g + 8][2t], D[g + 8][2t + 1], with the inner index of entry s of A and
+// B at t + 4 s; any other order of the inner index that A and B share gives the same product.
+__device__ __forceinline__ void mma_f64(double (&d)[4], const double (&a)[8], const double (&b)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f64.f64.f64.f64 {%0, %1, %2, %3}, {%4, %5, %6, %7, %8, %9, %10, %11}, "
+      "{%12, %13, %14, %15}, {%0, %1, %2, %3};"
+      : "+d"(d[0]), "+d"(d[1]), "+d"(d[2]), "+d"(d[3])
+      : "d"(a[0]), "d"(a[1]), "d"(a[2]), "d"(a[3]), "d"(a[4]), "d"(a[5]), "d"(a[6]), "d"(a[7]), "d"(b[0]), "d"(b[1]),
+        "d"(b[2]), "d"(b[3]));
+}
+
+constexpr int kSelectThreads = 256;
+
+// A CTA per QR query blocks of one head (QR <= 16: the rest of the product's rows are zero).
 template <int DH, int QR>
-__global__ void __launch_bounds__(256, 2) select_kernel(const SelectArgs a, const Means m, int tiles, int parts) {
+__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectArgs a, const Means m, int stride) {
   griddep_wait();
   griddep_launch_dependents();
   extern __shared__ double2 smem_select[];
-  double* qs = reinterpret_cast<double*>(smem_select);  // [DH][QR]
-  double* score = qs + DH * QR;                         // [QR][nkb_even], then the scores' order in the same place
+  constexpr int QS = DH + 2;  // padded row: 16-byte reads of neighbouring rows fall in distinct banks
+  double* qs = reinterpret_cast<double*>(smem_select);  // [16][QS]
+  double* score = qs + 16 * QS;                         // [QR][stride], then the scores' order in the same place
   unsigned long long* keys = reinterpret_cast<unsigned long long*>(score);
   const int i0 = blockIdx.x * QR, row = blockIdx.y;
   const int b = row / a.n_heads, h = row - b * a.n_heads;
   const int kvrow = b * a.n_kv_heads + h / (a.n_heads / a.n_kv_heads);
   const int qn = clamp_len(a.q_lens, b, a.Lq), kn = clamp_len(a.kv_lens, b, a.Lk);
   const int cand = (kn + a.block_k - 1) / a.block_k;  // key blocks that hold a valid key
-  const int nke = m.nkb_even;
+  const int nke = stride;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll 8
-  for (int x = threadIdx.x; x < DH * QR; x += blockDim.x) {
+#pragma unroll
+  for (int x = 2 * threadIdx.x; x < 16 * DH; x += 2 * kSelectThreads) {
     const int i = x / DH, e = x - i * DH;
     const long long at = ((long long)row * a.nqb + i0 + i) * DH + e;
-    qs[e * QR + i] = i0 + i < a.nqb && H3B_IDX_OK(at, m.nq, a.err) ? __ldg(m.q + at) : 0.0;
+    const bool on = i < QR && i0 + i < a.nqb && H3B_IDX_OK(at + 1, m.nq, a.err);
+    *reinterpret_cast<double2*>(qs + i * QS + e) = on ? __ldg(reinterpret_cast<const double2*>(m.q + at)) : make_double2(0.0, 0.0);
   }
   __syncthreads();
-  const int part = warp / tiles, len = DH / parts, e_first = part * len;
-  const double* km = m.k + (size_t)kvrow * DH * nke + (size_t)e_first * nke;
-  constexpr int EB = 4;  // lanes of the head per batch; len is a multiple of 2 EB
-  for (int base = 0; base < cand; base += 64 * tiles) {
-    const int j = base + 64 * (warp - part * tiles) + 2 * lane;  // keys j, j + 1 of this thread
-    const bool mine = j < cand;
-    double s0[QR], s1[QR];
+  const double* km = m.k + (size_t)kvrow * a.nkb * DH;
+  const int g = lane >> 2, t = lane & 3;
+  for (int j0 = 8 * warp; j0 < cand; j0 += kSelectThreads / 4) {  // eight keys of this warp
+    // the lane's whole column, requested at once: inner index 16 k + 4 t + s
+    double bk[DH / 16][4];
+    const double* kj = km + (size_t)min(j0 + g, cand - 1) * DH + 4 * t;
 #pragma unroll
-    for (int i = 0; i < QR; ++i) s0[i] = s1[i] = 0.0;
-    const double* kj = km + (mine ? j : 0);
-    auto fetch = [&](int e0, double2(&kk)[EB]) {
-#pragma unroll
-      for (int e = 0; e < EB; ++e) kk[e] = __ldg(reinterpret_cast<const double2*>(kj + (size_t)(e0 + e) * nke));
-    };
-    auto add = [&](int e0, const double2(&kk)[EB]) {
-#pragma unroll
-      for (int e = 0; e < EB; ++e)
-#pragma unroll
-        for (int i = 0; i < QR; i += 2) {
-          const double2 q2 = *reinterpret_cast<const double2*>(qs + (e_first + e0 + e) * QR + i);
-          s0[i] = fma(q2.x, kk[e].x, s0[i]);
-          s1[i] = fma(q2.x, kk[e].y, s1[i]);
-          s0[i + 1] = fma(q2.y, kk[e].x, s0[i + 1]);
-          s1[i + 1] = fma(q2.y, kk[e].y, s1[i + 1]);
-        }
-    };
-    double2 ka[EB], kb[EB];
-    fetch(0, ka);
-#pragma unroll 1
-    for (int e0 = 0; e0 < len; e0 += 2 * EB) {
-      fetch(e0 + EB, kb);
-      add(e0, ka);
-      if (e0 + 2 * EB < len) fetch(e0 + 2 * EB, ka);
-      add(e0 + EB, kb);
+    for (int k = 0; k < DH / 16; ++k) {
+      const double2 u = __ldg(reinterpret_cast<const double2*>(kj + 16 * k));
+      const double2 v = __ldg(reinterpret_cast<const double2*>(kj + 16 * k + 2));
+      bk[k][0] = u.x; bk[k][1] = u.y; bk[k][2] = v.x; bk[k][3] = v.y;
     }
-    for (int r = 0; r < parts; ++r) {
-      if (part == r && mine) {
+    double d[4] = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-        for (int i = 0; i < QR; ++i) {
-          double2* to = reinterpret_cast<double2*>(score + i * nke + j);
-          double2 v = make_double2(s0[i], s1[i]);
-          if (r > 0) {
-            const double2 w = *to;
-            v = make_double2(w.x + v.x, w.y + v.y);
-          }
-          *to = v;
+    for (int k = 0; k < DH / 16; ++k) {
+      double ak[8];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int s = 0; s < 4; s += 2) {
+          const double2 q2 = *reinterpret_cast<const double2*>(qs + (g + 8 * r) * QS + 16 * k + 4 * t + s);
+          ak[2 * s + r] = q2.x;
+          ak[2 * s + 2 + r] = q2.y;
         }
-      }
-      if (parts > 1) __syncthreads();
+      mma_f64(d, ak, bk[k]);
     }
+    if (g < QR) *reinterpret_cast<double2*>(score + g * nke + j0 + 2 * t) = make_double2(d[0], d[1]);
+    if (g + 8 < QR) *reinterpret_cast<double2*>(score + (g + 8) * nke + j0 + 2 * t) = make_double2(d[2], d[3]);
   }
   __syncthreads();
-  for (int i = warp; i < QR && i0 + i < a.nqb; i += blockDim.x >> 5) {
+  for (int i = warp; i < QR && i0 + i < a.nqb; i += kSelectThreads / 32) {
     const int n = (i0 + i) * kSparseQueries < qn ? cand : 0;
     const int want = min(n, a.topk);
     unsigned long long* key = keys + i * nke;
@@ -264,26 +255,23 @@ __global__ void __launch_bounds__(256, 2) select_kernel(const SelectArgs a, cons
 
 template <int DH, int QR>
 cudaError_t launch_select(const SelectArgs& a, const Means& m, cudaStream_t st) {
-  const size_t smem = sizeof(double) * ((size_t)DH * QR + (size_t)QR * m.nkb_even);
+  const int stride = (a.nkb + 7) & ~7;
+  const size_t smem = sizeof(double) * (16 * (size_t)(DH + 2) + (size_t)QR * stride);
   auto k = select_kernel<DH, QR>;
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int tiles = min((m.nkb_even + 63) / 64, 8);
-  const int parts = tiles == 1 ? 8 : tiles == 2 ? 4 : tiles <= 4 ? 2 : 1;
-  return launch_pdl(k, dim3((a.nqb + QR - 1) / QR, a.B * a.n_heads), dim3(32 * tiles * parts), smem, st, a, m, tiles, parts);
+  return launch_pdl(k, dim3((a.nqb + QR - 1) / QR, a.B * a.n_heads), dim3(kSelectThreads), smem, st, a, m, stride);
 }
 
 template <int DH>
-cudaError_t launch(const SelectArgs& a, int sms, cudaStream_t st) {
+cudaError_t launch(const SelectArgs& a, cudaStream_t st) {
   const Means m = means_of(a.ws, a.B, a.n_heads, a.n_kv_heads, DH, a.nqb, a.nkb);
   const long long blocks = (long long)a.B * a.n_heads * a.nqb + (long long)a.B * a.n_kv_heads * a.nkb;
   const dim3 grid((unsigned)((blocks + kMeanThreads / 32 - 1) / (kMeanThreads / 32)));
   const cudaError_t e = launch_pdl(block_means_kernel<DH>, grid, dim3(kMeanThreads), 0, st, a, m);
   if (e != cudaSuccess) return e;
-  // 16 query blocks a CTA read each key mean once for 16 products; fewer where that leaves
-  // processors without work, or where 16 rows of scores do not fit the shared memory
-  const long long ctas16 = (long long)a.B * a.n_heads * ((a.nqb + 15) / 16);
-  if (ctas16 >= sms && m.nkb_even <= 1280) return launch_select<DH, 16>(a, m, st);
+  // rows of scores that fit the shared memory
+  if (a.nkb <= 1536) return launch_select<DH, 16>(a, m, st);
   return launch_select<DH, 4>(a, m, st);
 }
 
@@ -295,7 +283,8 @@ size_t select_ws_bytes(int B, int n_heads, int n_kv_heads, int head_dim, int nqb
 }
 
 cudaError_t launch_select_blocks(const SelectArgs& a, int sms, cudaStream_t st) {
-  return a.head_dim == 128 ? launch<128>(a, sms, st) : launch<64>(a, sms, st);
+  (void)sms;
+  return a.head_dim == 128 ? launch<128>(a, st) : launch<64>(a, st);
 }
 
 }  // namespace h3b
