@@ -7,8 +7,8 @@
 // Two kernels. The means read q and k once, 16 bytes a lane, and are bound by
 // HBM. The scores are a product in 64 bits, [16 query blocks] x [all key blocks]
 // per CTA, on the FP64 matrix instruction (16 x 8 x 16), whose key means come
-// from L2; the topk of a row is found by a warp, by bisection over the bits of
-// the scores mapped to unsigned integers.
+// from L2; the topk of a row is found by a warp, by histograms over the scores
+// mapped to unsigned integers.
 #include "h3b_common.cuh"
 #include "h3b_internal.h"
 
@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
   griddep_wait();
   griddep_launch_dependents();
   extern __shared__ double2 smem_select[];
+  __shared__ __align__(16) unsigned hist[kSelectThreads / 32][256];
   constexpr int QS = DH + 2;  // padded row: 16-byte reads of neighbouring rows fall in distinct banks
   double* qs = reinterpret_cast<double*>(smem_select);  // [16][QS]
   double* score = qs + 16 * QS;                         // [QR][stride], then the scores' order in the same place
@@ -147,7 +148,6 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
   const int kvrow = b * a.n_kv_heads + h / (a.n_heads / a.n_kv_heads);
   const int qn = clamp_len(a.q_lens, b, a.Lq), kn = clamp_len(a.kv_lens, b, a.Lk);
   const int cand = (kn + a.block_k - 1) / a.block_k;  // key blocks that hold a valid key
-  const int nke = stride;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int x = 2 * threadIdx.x; x < 16 * DH; x += 2 * kSelectThreads) {
@@ -183,72 +183,127 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
         }
       mma_f64(d, ak, bk[k]);
     }
-    if (g < QR) *reinterpret_cast<double2*>(score + g * nke + j0 + 2 * t) = make_double2(d[0], d[1]);
-    if (g + 8 < QR) *reinterpret_cast<double2*>(score + (g + 8) * nke + j0 + 2 * t) = make_double2(d[2], d[3]);
+    if (g < QR) *reinterpret_cast<double2*>(score + g * stride + j0 + 2 * t) = make_double2(d[0], d[1]);
+    if (g + 8 < QR) *reinterpret_cast<double2*>(score + (g + 8) * stride + j0 + 2 * t) = make_double2(d[2], d[3]);
   }
   __syncthreads();
   for (int i = warp; i < QR && i0 + i < a.nqb; i += kSelectThreads / 32) {
     const int n = (i0 + i) * kSparseQueries < qn ? cand : 0;
     const int want = min(n, a.topk);
-    unsigned long long* key = keys + i * nke;
-    // the scores' order, and what bits all of it share
-    const int lo = (i0 + i) * kSparseQueries / a.block_k - a.keep_local + 1;
-    const int hi = ((i0 + i) * kSparseQueries + kSparseQueries - 1) / a.block_k + a.keep_local - 1;
-    unsigned long long all_or = 0ull, all_and = ~0ull;
-    for (int j = lane; j < n; j += 32) {
-      const bool keep = j < a.keep_first || (a.keep_local > 0 && j >= lo && j <= hi);
-      const unsigned long long v = keep ? kKeyKeep : order_key(score[i * nke + j]);
-      key[j] = v;
-      all_or |= v;
-      all_and &= v;
-    }
-    __syncwarp();
-    const unsigned long long differ = ((unsigned long long)__reduce_or_sync(0xFFFFFFFFu, (unsigned)((all_or ^ all_and) >> 32)) << 32) |
-                                      __reduce_or_sync(0xFFFFFFFFu, (unsigned)(all_or ^ all_and));
-    // every lane's own keys may agree among themselves and differ from another lane's
-    const unsigned long long any = ((unsigned long long)__reduce_or_sync(0xFFFFFFFFu, (unsigned)(all_or >> 32)) << 32) |
-                                   __reduce_or_sync(0xFFFFFFFFu, (unsigned)all_or);
-    const unsigned long long every = ((unsigned long long)__reduce_and_sync(0xFFFFFFFFu, (unsigned)(all_and >> 32)) << 32) |
-                                     __reduce_and_sync(0xFFFFFFFFu, (unsigned)all_and);
-    const unsigned long long mixed = differ | (any ^ every);  // bits in which two keys differ
-    const int top = 63 - __clzll((long long)mixed);           // the highest of them, -1: none
-    // the largest T with at least `want` keys >= T, bit by bit; done early when exactly `want` are
-    unsigned long long T = top < 0 ? any : top == 63 ? 0ull : any & ~((2ull << top) - 1ull);
-    int above = n;  // keys >= T
-    for (int bit = top; bit >= 0 && above > want; --bit) {
-      const unsigned long long c = T | (1ull << bit);
-      int cnt = 0;
-      for (int j = lane; j < n; j += 32) cnt += key[j] >= c;
-      cnt = __reduce_add_sync(0xFFFFFFFFu, cnt);
-      if (cnt >= want) {
-        T = c;
-        above = cnt;
-      }
-    }
-    // above > want: the keys equal to T are more than needed; the lowest of them are listed
-    int ties = above;
-    if (above > want) {
-      int more = 0;
-      for (int j = lane; j < n; j += 32) more += key[j] > T;
-      ties = want - __reduce_add_sync(0xFFFFFFFFu, more);
-    }
     const long long list = (long long)row * a.nqb + i0 + i;
     int* out = a.blocks + list * a.topk;
-    int at = 0, seen = 0;  // listed, and equal to T, so far
-    for (int j0 = 0; j0 < n && at < want; j0 += 32) {
-      const int j = j0 + lane;
-      const unsigned long long mine = j < n ? key[j] : 0ull;
-      const bool equal = j < n && mine == T;
-      const unsigned below = (1u << lane) - 1u;
-      const unsigned eq = __ballot_sync(0xFFFFFFFFu, equal);
-      const bool take = j < n && (mine > T || (equal && seen + __popc(eq & below) < ties));
+    const int lo_kept = (i0 + i) * kSparseQueries / a.block_k - a.keep_local + 1;
+    const int hi_kept = ((i0 + i) * kSparseQueries + kSparseQueries - 1) / a.block_k + a.keep_local - 1;
+    auto key_of = [&](int j) {
+      const bool keep = j < a.keep_first || (a.keep_local > 0 && j >= lo_kept && j <= hi_kept);
+      return keep ? kKeyKeep : order_key(score[i * stride + j]);
+    };
+    const unsigned below = (1u << lane) - 1u;
+    if (n <= 32) {  // a key per lane: its rank by comparison with all
+      const unsigned long long mine = lane < n ? key_of(lane) : 0ull;  // every key is above zero
+      int rank = 0;
+#pragma unroll
+      for (int o = 0; o < 32; ++o) {
+        const unsigned long long other = __shfl_sync(0xFFFFFFFFu, mine, o);
+        rank += other > mine || (other == mine && o < lane);
+      }
+      const bool take = lane < n && rank < want;
       const unsigned tk = __ballot_sync(0xFFFFFFFFu, take);
-      const int to = at + __popc(tk & below);
-      if (take && H3B_IDX_OK(to, want, a.err)) out[to] = j;
-      at += __popc(tk);
-      seen += __popc(eq);
+      if (take && H3B_IDX_OK(__popc(tk & below), want, a.err)) out[__popc(tk & below)] = lane;
+    } else {
+      // The threshold T: all keys above it, and the first `ties` of those equal to it, are listed. A
+      // histogram of 256 bins over the keys' range finds the bin that the want-th key lies in, which is
+      // the next range; done when the bin is taken whole. Kept blocks are counted apart: their key
+      // is not a score, and would stretch the range.
+      unsigned long long* key = keys + i * stride;
+      unsigned top = 0u, bottom = ~0u;
+      int kept = 0;
+      for (int j = lane; j < n; j += 32) {
+        const unsigned long long v = key_of(j);
+        key[j] = v;
+        if (v == kKeyKeep) {
+          ++kept;
+        } else {
+          top = max(top, (unsigned)(v >> 32));
+          bottom = min(bottom, (unsigned)(v >> 32));
+        }
+      }
+      kept = __reduce_add_sync(0xFFFFFFFFu, kept);
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      bottom = __reduce_min_sync(0xFFFFFFFFu, bottom);
+      unsigned long long T = kKeyKeep;
+      int ties = n, need = want - kept;
+      if (need > 0) {
+        unsigned long long lo = (unsigned long long)bottom << 32;
+        // the range is a power of two above (top - bottom + 1) 2^32, 256 bins of 2^sh
+        int sh = max(0, 64 - __clzll((long long)(((unsigned long long)(top - bottom) << 32) | 0xFFFFFFFFull)) - 8);
+        unsigned* bins = hist[warp];
+        for (;;) {
+          for (int x = lane; x < 64; x += 32) reinterpret_cast<uint4*>(bins)[x] = make_uint4(0, 0, 0, 0);
+          __syncwarp();
+          for (int j = lane; j < n; j += 32) {
+            const unsigned long long v = key[j], d = v - lo;
+            if (v != kKeyKeep && v >= lo && (d >> sh) < 256ull) atomicAdd(bins + (unsigned)(d >> sh), 1u);
+          }
+          __syncwarp();
+          // this lane's eight bins, and the keys in bins above them
+          const uint4 p = reinterpret_cast<const uint4*>(bins)[2 * lane], q = reinterpret_cast<const uint4*>(bins)[2 * lane + 1];
+          const unsigned c[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+          unsigned sum = 0;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) sum += c[x];
+          unsigned upto = sum;  // of this lane and those above
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned u = __shfl_down_sync(0xFFFFFFFFu, upto, o);
+            if (lane + o < 32) upto += u;
+          }
+          unsigned over = upto - sum;  // in the bins above the one found
+          int bin = 0;
+          unsigned in = 0;
+          const bool here = over < (unsigned)need && (unsigned)need <= upto;  // one lane
+          if (here) {
+            bool found = false;
+#pragma unroll
+            for (int x = 7; x >= 0; --x) {
+              if (!found && over + c[x] >= (unsigned)need) {
+                found = true;
+                bin = 8 * lane + x;
+                in = c[x];
+              }
+              if (!found) over += c[x];
+            }
+          }
+          const int src = __ffs(__ballot_sync(0xFFFFFFFFu, here)) - 1;
+          bin = __shfl_sync(0xFFFFFFFFu, bin, src);
+          in = __shfl_sync(0xFFFFFFFFu, in, src);
+          need -= (int)__shfl_sync(0xFFFFFFFFu, over, src);
+          T = lo + ((unsigned long long)bin << sh);
+          if ((int)in == need) break;  // the whole bin: every key >= T
+          if (sh == 0) {               // equal keys, more than needed
+            ties = need;
+            break;
+          }
+          lo = T;
+          sh = max(0, sh - 8);
+        }
+        if (ties == n) T -= 1;  // keys >= T, as keys above T - 1 (T > 0: no key is zero)
+      }
+      int at = 0, seen = 0;  // listed, and equal to T, so far
+      for (int j0 = 0; j0 < n && at < want; j0 += 32) {
+        const int j = j0 + lane;
+        const unsigned long long mine = j < n ? key[j] : 0ull;
+        const bool equal = ties < n && j < n && mine == T;
+        const unsigned eq = __ballot_sync(0xFFFFFFFFu, equal);
+        const bool take = j < n && (mine > T || mine == kKeyKeep || (equal && seen + __popc(eq & below) < ties));
+        const unsigned tk = __ballot_sync(0xFFFFFFFFu, take);
+        const int to = at + __popc(tk & below);
+        if (take && H3B_IDX_OK(to, want, a.err)) out[to] = j;
+        at += __popc(tk);
+        seen += __popc(eq);
+      }
     }
-    for (int t = want + lane; t < a.topk; t += 32) out[t] = -1;
+    for (int x = want + lane; x < a.topk; x += 32) out[x] = -1;
     if (lane == 0) a.counts[list] = want;
   }
 }
