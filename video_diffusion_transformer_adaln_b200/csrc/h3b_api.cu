@@ -404,6 +404,17 @@ bool make_tmap_3d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t d
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_4d_bf16(CUtensorMap* map, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                       const uint32_t (&box)[4]) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]}, s[3] = {strides[0], strides[1], strides[2]};
+  const cuuint32_t bx[4] = {box[0], box[1], box[2], box[3]}, estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, s, bx, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace h3b
 
 using namespace h3b;
@@ -910,6 +921,7 @@ h3b_status h3b_qk_norm_rope(const h3b_qk_dims* dims, const void* qkv, const floa
   const long long width = (long long)(d.n_heads + 2 * d.n_kv_heads) * d.head_dim;
   if (d.row_stride < width || d.row_stride % 8 != 0 || d.row_stride > (1LL << 31))
     return fail(H3B_ERR_SHAPE, "row_stride must be a multiple of 8, at least (n_heads + 2 n_kv_heads) * head_dim");
+  if (d.L * d.row_stride > (1LL << 38)) return fail(H3B_ERR_SHAPE, "an item of the projection exceeds 2^38 elements");
   if ((long long)d.B * d.L == 0) return H3B_OK;  // empty problem: nothing to launch
   if (!qkv || !q || !k || !v) return fail(H3B_ERR_ARG, "NULL pointer");
   if (!aligned16(qkv) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(wq) || !aligned16(wk) ||
