@@ -171,3 +171,21 @@ def test_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         h3b.h3b_qk_norm_rope(d, qkv, wq, wk, pos, *want)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("B,L,H,KV,dh,rope,pad", [
+    (2, 4201, 18, 6, 128, (32, 48, 48), 8),   # many boxes per CTA; heads and tokens cut a box
+    (3, 5003, 21, 7, 64, (16, 24, 24), 0),
+])
+def test_many_boxes(B, L, H, KV, dh, rope, pad):
+    require_gpu()
+    qkv, wq, wk, pos = make(B, L, H, KV, dh, pad, fractional=True)
+    bufs = [torch.full((B * h * L * dh + 128,), 5.0, dtype=torch.bfloat16, device="cuda") for h in (H, KV, KV)]
+    got = [b[64:-64].view(B, h, L, dh) for b, h in zip(bufs, (H, KV, KV))]
+    h3b.h3b_qk_norm_rope(h3b.make_qk(B, L, H, KV, dh, rope, row_stride=qkv.shape[1]), qkv, wq, wk, pos, *got)
+    ref, mag = R.qk_norm_rope(qkv, B, L, H, KV, dh, rope, wq, wk, pos)
+    check(got, ref, mag)
+    assert torch.equal(got[2].double(), ref[2])
+    for b in bufs:
+        assert (b[:64] == 5.0).all() and (b[-64:] == 5.0).all()
+    no_device_error()

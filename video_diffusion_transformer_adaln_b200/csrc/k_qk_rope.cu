@@ -30,7 +30,7 @@ constexpr int kHeads = 4;                    // heads per box
 constexpr int kSlots = 6;
 constexpr int kBoxBytes = 16384;
 constexpr size_t kSmem = (size_t)kSlots * kBoxBytes + 3 * kSlots * 8 + 16 + 128;
-constexpr int kCtasPerSm = 2;                // by registers and shared memory (4 slots: 206 us where 6 take 184)
+constexpr int kCtasPerSm = 2;                // by registers and shared memory
 
 // (cos, sin) of pair p at this token. The angle in half turns is reduced to
 // [-1, 1] in 64 bits before it is rounded to 32, so its error is that of a
