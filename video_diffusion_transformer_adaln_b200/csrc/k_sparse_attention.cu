@@ -70,8 +70,9 @@ struct Layout {
   static constexpr int Q_OFF = 0, RING_OFF = 2 * TILE;
   static constexpr int BAR_OFF = RING_OFF + NS * TILE;
   // mbarriers, by their place: per item (two each), per slot, per pair in flight
-  static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FULL = 4, P_FULL = 6, FIN = 8, FULL = 10, EMPTY = FULL + NS;
-  static constexpr int PAIR_FULL = EMPTY + NS, PAIR_EMPTY = PAIR_FULL + kPairs, CANCEL = PAIR_EMPTY + kPairs;
+  static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FIRST = 4, P_FULL = 6, FIN = 8, FULL = 10, EMPTY = FULL + NS;
+  static constexpr int PAIR_FULL = EMPTY + NS, PAIR_EMPTY = PAIR_FULL + kPairs, CLEAN = PAIR_EMPTY + kPairs;
+  static constexpr int CANCEL = CLEAN + kPairs;
   static constexpr int DRAIN = CANCEL + 1, NBARS = DRAIN + 1;
   static constexpr int FLAG_OFF = BAR_OFF + (NBARS + 1) / 2 * 16;  // tensor memory address, abort flag, loads
   static constexpr int RESPONSE_OFF = FLAG_OFF + 16;               // of the take-over request
@@ -102,6 +103,14 @@ __device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t units) {
   return (d & 0xFFFFFFFF00000000ull) | r;
 }
 
+// A copy of its own for each role. A value that lives in all of them is kept on the stack while the softmax
+// needs the registers, and would be reloaded at each of its uses between the MMAs.
+__device__ __forceinline__ uint32_t own_copy(uint32_t v) {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 // What an item works on. Kept in shared memory: the softmax threads' registers are the scores'.
 struct Item {
   int bh, qb;     // batch item x head, query block
@@ -109,14 +118,13 @@ struct Item {
   int qn, kn;     // valid queries and keys of the batch item
   int t0, units;  // first tile of the range, units in it
   int tiles;      // ceil(units / 2); -1: no further pair
-  int clean;      // every unit of the range holds 64 valid keys
+  int clean;      // every unit of the range holds 64 valid keys (written after the rest)
   int pad;
   const int* list;
 };
 static_assert(sizeof(Item) <= kItemBytes && kItemBytes % 8 == 0, "the items' place in shared memory");
 
-// By a whole warp.
-__device__ __forceinline__ Item load_item(const SparseParams& p, int item, int lane) {
+__device__ __forceinline__ Item load_item(const SparseParams& p, int item) {
   const SparseAttnArgs& a = p.a;
   Item it{};
   if (item >= p.rows * p.nsplit) return it;
@@ -129,18 +137,22 @@ __device__ __forceinline__ Item load_item(const SparseParams& p, int item, int l
   it.kn = clamp_len(a.kv_lens, b, a.Lk);
   it.list = a.blocks + (size_t)row * a.topk;
   const int entries = a.counts ? min(max(__ldg(a.counts + row), 0), a.topk) : a.topk;
-  const int per = a.block_k / kUnit;  // units per entry
-  const int all = it.qb * kSparseQueries < it.qn && it.kn > 0 ? entries * per : 0;
+  const int all = it.qb * kSparseQueries < it.qn && it.kn > 0 ? entries * (a.block_k / kUnit) : 0;
   it.t0 = split * p.split_tiles;
   it.units = min(max(all - 2 * it.t0, 0), 2 * p.split_tiles);
   it.tiles = (it.units + 1) / 2;
+  return it;
+}
+
+// Whether every unit of the item's range holds 64 valid keys. By a whole warp.
+__device__ __forceinline__ int all_clean(const SparseAttnArgs& a, const Item& it, int lane) {
+  const int per = a.block_k / kUnit;  // units per entry
   bool clean = true;
   for (int u = lane * per; u < it.units; u += 32 * per) {
     const int v = __ldg(it.list + (2 * it.t0 + u) / per);
     clean = clean && (unsigned)v < (unsigned)a.nkb && (v + 1) * a.block_k <= it.kn;
   }
-  it.clean = __all_sync(0xFFFFFFFFu, clean);
-  return it;
+  return __all_sync(0xFFFFFFFFu, clean);
 }
 
 // Walks an item's list in tiles; a warp's lanes hold 32 entries as the first keys of their blocks
@@ -208,6 +220,19 @@ __device__ __forceinline__ bool wait_reached(const volatile uint32_t* count, uin
   }
 }
 
+// The same in one register, for the softmax threads: the number of the load modulo 2 NS.
+template <int NS>
+struct Turn {
+  int c = 0;
+  __device__ __forceinline__ int slot() const { return c < NS ? c : c - NS; }
+  __device__ __forceinline__ uint32_t ph() const { return c < NS ? 0u : 1u; }
+  __device__ __forceinline__ void advance(int by) {  // by <= 2 NS
+    c += by;
+    if (c >= 2 * NS) c -= 2 * NS;
+  }
+  __device__ __forceinline__ void advance_any(int by) { c = (c + by) % (2 * NS); }
+};
+
 // Asks for the takeover of a CTA of this grid that has not started; the 16-byte response completes on `bar`.
 __device__ __forceinline__ void request_cta(uint32_t response, uint32_t bar) {
   asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
@@ -239,10 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const SparseAttnArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t sb = smem_u32(smem);
-  auto bar = [&](int place) { return sb + Lay::BAR_OFF + 8u * place; };
+  const uint32_t sb_ = smem_u32(smem);
+  auto bar = [&](int place) { return sb_ + Lay::BAR_OFF + 8u * place; };
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + Lay::FLAG_OFF);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Lay::FLAG_OFF + 4);
   volatile uint32_t* loaded = reinterpret_cast<volatile uint32_t*>(smem + Lay::FLAG_OFF + 8);  // each producer's last load
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr uint32_t IDESC_S = instr_desc(1, 1, 0, 0, kSparseQueries, kTile);
@@ -253,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < Lay::NBARS; ++i) mbar_init(bar(i), 1);
     for (int g = 0; g < 2; ++g) mbar_init(bar(Lay::P_FULL + g), 4);                  // softmax warps of an item
     for (int i = 0; i < kPairs; ++i) mbar_init(bar(Lay::PAIR_EMPTY + i), 2 + 1 + 8);  // producers, MMA, softmax warps
-    *abort_flag = 0;
+    *reinterpret_cast<volatile int*>(smem + Lay::FLAG_OFF + 4) = 0;
     loaded[0] = loaded[1] = ~0u;
     fence_barrier_init();
     tma_prefetch_desc(&tmq);
@@ -261,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmv);
   }
   if (warp == 1) {
-    tmem_alloc(sb + Lay::FLAG_OFF, kTmemCols);
+    tmem_alloc(sb_ + Lay::FLAG_OFF, kTmemCols);
     tmem_relinquish();
     tc_fence_before();
   }
@@ -270,12 +294,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();  // q, k, v and the lists may be the previous grid's output
   griddep_launch_dependents();
 
+  auto flag_at = [](uint32_t base) { return static_cast<volatile int*>(__cvta_shared_to_generic(base + Lay::FLAG_OFF + 4)); };
   // Pair k of this CTA, in every role: its items once they are there (nullptr after a failure).
   // `lanes`: those that call it, which decide as one (they may see the abort flag at different times).
-  auto pair_items = [&](int k, unsigned lanes) -> const Item* {
-    const bool ok = mbar_wait_or_abort(bar(Lay::PAIR_FULL + k % kPairs), (k / kPairs) & 1, abort_flag, a.err, ERR_WAIT_EPI);
+  auto pair_items = [&](uint32_t base, int k, unsigned lanes) -> const Item* {
+    const bool ok = mbar_wait_or_abort(base + Lay::BAR_OFF + 8u * (Lay::PAIR_FULL + k % kPairs), (k / kPairs) & 1,
+                                       flag_at(base), a.err, ERR_WAIT_EPI);
     if (!__all_sync(lanes, ok)) return nullptr;
-    return reinterpret_cast<const Item*>(smem + Lay::ITEM_OFF + (k % kPairs) * 2 * kItemBytes);
+    return static_cast<const Item*>(__cvta_shared_to_generic(base + Lay::ITEM_OFF + (k % kPairs) * 2 * kItemBytes));
   };
   auto second = [](const Item* it) {
     return reinterpret_cast<const Item*>(reinterpret_cast<const uint8_t*>(it) + kItemBytes);
@@ -285,6 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsControl));
     if (warp == 0 || warp == 2) {
       // ---------------- TMA producer of item g (whole warp; lane 0 issues)
+      const uint32_t sb = own_copy(sb_);
+      auto bar = [&](int place) { return sb + Lay::BAR_OFF + 8u * place; };
+      volatile int* abort_flag = flag_at(sb);
       const int g = warp >> 1;
       Place<NS> place;                  // of the pair's first load
       uint32_t last = ~0u;              // number of this warp's load before; none yet: the one before the first
@@ -316,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       for (int k = 0; ok; ++k) {
-        const Item* pair = pair_items(k, 0xFFFFFFFFu);
+        const Item* pair = pair_items(sb, k, 0xFFFFFFFFu);
         if (!pair) { ok = false; break; }
         const int n0 = pair->tiles, n1 = second(pair)->tiles;
         if (n0 < 0) break;
@@ -325,16 +354,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         Place<NS> at = place;
         place.advance_any(2 * (n0 + n1));
         if (n > 0) {
-          ListWalk walk;
-          walk.block_k = a.block_k;
-          walk.nkb = a.nkb;
-          walk.none = a.nkb * a.block_k;  // >= Lk: rows there read as zeros
-          walk.kn = it->kn;
-          walk.list = it->list + (a.block_k == kTile ? it->t0 : 2 * it->t0);
-          walk.entries = a.block_k == kTile ? (units + 1) / 2 : units;
-          walk.base = 0;
-          walk.cur = walk.fetch(lane);
-          walk.nxt = walk.fetch(32 + lane);
           // Q, once the item before is done with its S products
           if (items_done > 0) {
             const bool free_ =
@@ -349,6 +368,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_3d(sb + Lay::Q_OFF + g * Lay::TILE + b * kBox, &tmq, bar(Lay::Q_FULL + g), b * 64,
                           it->qb * kSparseQueries, it->bh);
           }
+          ListWalk walk;
+          walk.block_k = a.block_k;
+          walk.nkb = a.nkb;
+          walk.none = a.nkb * a.block_k;  // >= Lk: rows there read as zeros
+          walk.kn = it->kn;
+          walk.list = it->list + (a.block_k == kTile ? it->t0 : 2 * it->t0);
+          walk.entries = a.block_k == kTile ? (units + 1) / 2 : units;
+          walk.base = 0;
+          walk.cur = walk.fetch(lane);
+          walk.nxt = walk.fetch(32 + lane);
           if (g == 1) at.advance(n0 > 0);
           int2 keys = walk.tile(0, units, lane);
           ok = load(&tmk, at, keys, units > 1, kvrow);
@@ -377,7 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       if (lane == 0) {
         // ---------------- MMA issuer
-        const uint32_t tm = *tmem_slot;
+        const uint32_t sb = own_copy(sb_), tm = *tmem_slot;
+        auto bar = [&](int place) { return sb + Lay::BAR_OFF + 8u * place; };
+        volatile int* abort_flag = flag_at(sb);
         bool any = false, ok = true;
         Place<NS> at;
         uint32_t tiles_done[2] = {0, 0}, items_done[2] = {0, 0};
@@ -389,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit(bar(Lay::EMPTY + at.slot));
           at.advance(1);
         };
-        auto issue_s = [&](int g, bool two, bool last) -> bool {  // S_g = Q_g K^T of the item's next tile
+        auto issue_s = [&](int g, bool two, bool first, bool last) -> bool {  // S_g = Q_g K^T of the item's next tile
           if (!take()) return false;
           tc_fence_after();
           const uint64_t qd = smem_desc_sw128(sb + Lay::Q_OFF + g * Lay::TILE, 16, 1024);
@@ -407,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_f16(tm + Lay::S_COL(g), desc_add(qd, step), desc_add(kd, step), IDESC_S_HALF, k > 0 ? 1u : 0u);
             }
           }
-          tc_commit(bar(Lay::S_FULL + g));
+          if (first) tc_commit(bar(Lay::S_FIRST + g));
           if (last) tc_commit(bar(Lay::Q_EMPTY + g));
           give();
           return true;
@@ -433,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           return true;
         };
         for (int k = 0; ok; ++k) {
-          const Item* pair = pair_items(k, 1u);
+          const Item* pair = pair_items(sb, k, 1u);
           if (!pair) { ok = false; break; }
           const int n0 = pair->tiles, n1 = second(pair)->tiles;
           if (n0 < 0) break;
@@ -443,12 +474,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (units == 0) return true;
             if (!mbar_wait_or_abort(bar(Lay::Q_FULL + g), items_done[g] & 1, abort_flag, a.err, ERR_WAIT_TMA)) return false;
             ++items_done[g];
-            return issue_s(g, units > 1, units <= 2);
+            return issue_s(g, units > 1, true, units <= 2);
           };
           auto round = [&](int g, int units, int n, int t) -> bool {
             if (t >= n) return true;
             if (!issue_pv(g, units - 2 * t > 1, t == 0)) return false;
-            if (t + 1 < n) return issue_s(g, units - 2 * (t + 1) > 1, t + 2 == n);
+            if (t + 1 < n) return issue_s(g, units - 2 * (t + 1) > 1, false, t + 2 == n);
             tc_commit(bar(Lay::FIN + g));
             return true;
           };
@@ -466,6 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       // ---------------- the next pair (whole warp)
+      const uint32_t sb = own_copy(sb_);
+      auto bar = [&](int place) { return sb + Lay::BAR_OFF + 8u * place; };
+      volatile int* abort_flag = flag_at(sb);
       int cta = blockIdx.x;
       bool ok = true;
       for (int k = 0; ok && cta >= 0; ++k) {
@@ -492,37 +526,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it0{}, it1{};
         it0.tiles = -1;
         if (cta >= 0) {
-          it0 = load_item(p, 2 * cta, lane);
-          it1 = load_item(p, 2 * cta + 1, lane);
+          it0 = load_item(p, 2 * cta);
+          it1 = load_item(p, 2 * cta + 1);
         }
+        Item* to = static_cast<Item*>(__cvta_shared_to_generic(sb + Lay::ITEM_OFF + (k % kPairs) * 2 * kItemBytes));
         if (lane == 0) {
-          Item* to = reinterpret_cast<Item*>(smem + Lay::ITEM_OFF + (k % kPairs) * 2 * kItemBytes);
           *to = it0;
           *const_cast<Item*>(second(to)) = it1;
           mbar_arrive(bar(Lay::PAIR_FULL + k % kPairs));
         }
         __syncwarp();
+        if (cta >= 0) {  // only the softmax asks, and not before the first tile
+          const int clean0 = all_clean(a, it0, lane), clean1 = all_clean(a, it1, lane);
+          if (lane == 0) {
+            to->clean = clean0;
+            const_cast<Item*>(second(to))->clean = clean1;
+            mbar_arrive(bar(Lay::CLEAN + k % kPairs));
+          }
+          __syncwarp();
+        }
       }
       if (!ok) *abort_flag = 1;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     // ---------------- softmax warps: 4-7 -> item 0, 8-11 -> item 1 (thread = query row)
+    const uint32_t sb = own_copy(sb_);
+    auto bar = [&](int place) { return sb + Lay::BAR_OFF + 8u * place; };
+    volatile int* abort_flag = flag_at(sb);
     const int g = (warp - 4) >> 2;
     const int quad = warp & 3;
     const int row = quad * 32 + lane;
     const uint32_t t_lane = (uint32_t)(quad * 32) << 16;
     const uint32_t s_col = *tmem_slot + t_lane + Lay::S_COL(g), o_col = *tmem_slot + t_lane + Lay::O_COL(g);
     const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
-    uint32_t tiles_done = 0, items_done = 0;
-    Place<NS> place;  // of the pair's first load
+    uint32_t items_done = 0;
+    Turn<NS> place;  // of the pair's first load
     bool ok = true;
     for (int k = 0; ok; ++k) {
-      const volatile Item* pair = pair_items(k, 0xFFFFFFFFu);
+      const volatile Item* pair = pair_items(sb, k, 0xFFFFFFFFu);
       if (!pair) { ok = false; break; }
       if (pair->tiles < 0) break;
+      const bool looked = mbar_wait_or_abort(bar(Lay::CLEAN + k % kPairs), (k / kPairs) & 1, abort_flag, a.err, ERR_WAIT_EPI);
+      if (!__all_sync(0xFFFFFFFFu, looked)) { ok = false; break; }
       const volatile Item* it = g ? second(const_cast<const Item*>(pair)) : pair;
-      const int tiles = it->tiles;
       const bool live = it->qb * kSparseQueries + quad * 32 < it->qn;  // warp-uniform: a valid row in this warp
       // valid keys of unit u (counted from the item's first): the entry's block ends at kv_len
       auto valid_keys = [&](int u) {
@@ -532,64 +579,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((unsigned)v >= (unsigned)a.nkb) return 0;
         return min(kUnit, max(0, it->kn - v * a.block_k - (wide ? (u & 1) * kUnit : 0)));
       };
-      // every tile but a last one of one unit holds 128 valid keys
-      const int whole = it->clean ? it->units / 2 : 0;
       float m_run = kNoMax, l_run = 0.0f;
-      for (int t = 0; t < tiles; ++t) {
+      const volatile Item* other = g ? pair : second(const_cast<const Item*>(pair));
+      Turn<NS> at = place;  // of K_g(t)
+      if (g == 1) at.advance(other->tiles > 0);
+      for (int t = 0; t < it->tiles; ++t) {
         int nv0 = kUnit, nv1 = kUnit;
-        if (t >= whole) {
+        if (!it->clean || 2 * t + 1 >= it->units) {  // a clean list's whole tiles hold 128 valid keys
           nv0 = valid_keys(2 * t);
           nv1 = valid_keys(2 * t + 1);
         }
-        const bool s_ok =
-            mbar_wait_or_abort(bar(Lay::S_FULL + g), tiles_done & 1, abort_flag, a.err, ERR_WAIT_MMA);
+        // S_g(t) is complete when its K is released: one commit tells both (each costs the tensor core some
+        // 40 cycles). The parity is of this use of the slot: K_g(t-1), at most four loads earlier, is released,
+        // so the use NS loads earlier is over, and the next one's release comes after P V of this tile, which waits
+        // for this warp. The first tile, which has no K_g(t-1) to go by, has a barrier of its own.
+        const uint32_t s_bar = t == 0 ? bar(Lay::S_FIRST + g) : bar(Lay::EMPTY + at.slot());
+        const bool s_ok = mbar_wait_or_abort(s_bar, t == 0 ? items_done & 1 : at.ph(), abort_flag, a.err, ERR_WAIT_MMA);
         if (!__all_sync(0xFFFFFFFFu, s_ok)) { ok = false; break; }
-        ++tiles_done;
+        // to V_g(t): past the other item's loads between (see the producers)
+        const int others = other->tiles;
+        at.advance(1 + (g == 0 ? (t > 0 && t - 1 < others) + (t < others) : (t < others) + (t + 1 < others)));
         // V rows behind kv_len (in memory, so TMA does not zero them) are zeroed once V_t has landed. S_g(t) is
         // complete, so every load up to K_g(t) has been used, among them the one that held V_g(t)'s
         // slot before (at least five loads earlier): the parity cannot be of an older phase
-        const bool cut0 = nv0 > 0 && nv0 < kUnit, cut1 = nv1 > 0 && nv1 < kUnit;
-        if ((cut0 || cut1) && it->kn < a.Lk) {
-          // place of V_g(t) in the order of loads: the first K tiles, the loads of the rounds
-          // before t, and item 0's loads of this round
-          const int n0 = pair->tiles, n1 = second(const_cast<const Item*>(pair))->tiles;
-          int pos = (n0 > 0) + (n1 > 0) + min(t, n0) + min(t, max(n0 - 1, 0)) + min(t, n1) + min(t, max(n1 - 1, 0));
-          if (g == 1) pos += (t < n0) + (t + 1 < n0);
-          Place<NS> at = place;
-          at.advance_any(pos);
-          const bool v_ok = mbar_wait_or_abort(bar(Lay::FULL + at.slot), at.ph, abort_flag, a.err, ERR_WAIT_TMA);
+        if (((nv0 > 0 && nv0 < kUnit) || (nv1 > 0 && nv1 < kUnit)) && it->kn < a.Lk) {
+          const bool v_ok = mbar_wait_or_abort(bar(Lay::FULL + at.slot()), at.ph(), abort_flag, a.err, ERR_WAIT_TMA);
           if (!__all_sync(0xFFFFFFFFu, v_ok)) { ok = false; break; }
           for (int u = 0; u < 2; ++u) {
-            if (!(u ? cut1 : cut0)) continue;
-            for (int x = (u ? nv1 : nv0) * 8 + row; x < kUnit * 8; x += 128)
+            const int nv = u ? nv1 : nv0;
+            if (nv == 0) continue;
+            for (int x = nv * 8 + row; x < kUnit * 8; x += 128)
               for (int b = 0; b < Lay::NBOX; ++b)
-                *reinterpret_cast<uint4*>(smem + Lay::RING_OFF + at.slot * Lay::TILE + b * kBox + u * kUnitBox + x * 16) =
+                *static_cast<uint4*>(__cvta_shared_to_generic(sb + Lay::RING_OFF + at.slot() * Lay::TILE + b * kBox + u * kUnitBox + x * 16)) =
                     make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
+        at.advance(1);  // to K_g(t + 1)
         if (live) {
           tc_fence_after();
           uint32_t sr[kTile];
-  #pragma unroll
+#pragma unroll
           for (int c = 0; c < kTile / 32; ++c)
             tmem_ld32(s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
           tmem_ld_wait();
-  #pragma unroll
+#pragma unroll
           for (int c = 0; c < kTile / 32; ++c) tmem_reg_fence(*reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
           if (nv0 < kUnit || nv1 < kUnit) {  // warp-uniform
-  #pragma unroll
+#pragma unroll
             for (int i = 0; i < kTile; ++i)
               if ((i & (kUnit - 1)) >= (i < kUnit ? nv0 : nv1)) sr[i] = __float_as_uint(-INFINITY);
           }
           // row max with 8 independent partial maxima; NaN if a score is (then the row's sum is NaN too,
           // whichever pipe computes that score's exponential)
           float pm[8];
-  #pragma unroll
+#pragma unroll
           for (int e = 0; e < 8; ++e) pm[e] = __uint_as_float(sr[e]);
-  #pragma unroll
+#pragma unroll
           for (int i = 8; i < kTile; i += 16)
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 8; ++e) pm[e] = max3_nan(pm[e], __uint_as_float(sr[i + e]), __uint_as_float(sr[i + 8 + e]));
           const float mx = max3_nan(max3_nan(pm[0], pm[1], pm[2]), max3_nan(pm[3], pm[4], pm[5]), max3_nan(pm[6], pm[7], kNoMax));
           // finite also where every key of the tile is masked, so that exp2(-inf - m) is 0; an infinite
@@ -607,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // p = exp2(s * c - m), packed to bf16 pairs in place; sum with 4 packed accumulators
           const float2 nm2 = make_float2(-m_run, -m_run);
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-  #pragma unroll
+#pragma unroll
           for (int i = 0; i < kTile; i += 2) {
             const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), c2, nm2);
             float2 e;
@@ -623,13 +671,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           l_run = fmaf(l_run, alpha, a03.x + a03.y);
           // S_g(t) complete => PV_g(t-1) complete: O_g is stable until P_g(t) is published.
           if (__any_sync(0xFFFFFFFFu, rescale)) {
-  #pragma unroll
+#pragma unroll
             for (int c = 0; c < DH / 32; ++c) {
               uint32_t o[32];
               tmem_ld32(o_col + c * 32, o);
               tmem_ld_wait();
               tmem_reg_fence(o);
-  #pragma unroll
+#pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
                                             make_float2(alpha, alpha));
@@ -649,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(Lay::P_FULL + g));
       }
       if (!ok) break;
-      if (tiles > 0) {
+      if (it->tiles > 0) {
         const bool f_ok = mbar_wait_or_abort(bar(Lay::FIN + g), items_done & 1, abort_flag, a.err, ERR_WAIT_MMA);
         if (!__all_sync(0xFFFFFFFFu, f_ok)) { ok = false; break; }
         ++items_done;
