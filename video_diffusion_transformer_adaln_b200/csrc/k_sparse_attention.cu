@@ -51,6 +51,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kUnitBox = kUnit * 128;  // bytes of 64 rows x 64 lanes
 constexpr int kBox = kTile * 128;      // bytes of 128 rows x 64 lanes
 constexpr int kPairs = 2;              // pairs of items in flight in a CTA
+constexpr int kAhead = 3;              // tiles before a pair's end at which the next is asked for
 constexpr int kItemBytes = 64;
 constexpr float kNoMax = -3.0e38f;     // running maximum before any key
 
@@ -72,7 +73,7 @@ struct Layout {
   // mbarriers, by their place: per item (two each), per slot, per pair in flight
   static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FIRST = 4, P_FULL = 6, FIN = 8, FULL = 10, EMPTY = FULL + NS;
   static constexpr int PAIR_FULL = EMPTY + NS, PAIR_EMPTY = PAIR_FULL + kPairs, CLEAN = PAIR_EMPTY + kPairs;
-  static constexpr int CANCEL = CLEAN + kPairs;
+  static constexpr int ENDING = CLEAN + kPairs, CANCEL = ENDING + 1;
   static constexpr int DRAIN = CANCEL + 1, NBARS = DRAIN + 1;
   static constexpr int FLAG_OFF = BAR_OFF + (NBARS + 1) / 2 * 16;  // tensor memory address, abort flag, loads
   static constexpr int RESPONSE_OFF = FLAG_OFF + 16;               // of the take-over request
@@ -277,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < Lay::NBARS; ++i) mbar_init(bar(i), 1);
     for (int g = 0; g < 2; ++g) mbar_init(bar(Lay::P_FULL + g), 4);                  // softmax warps of an item
     for (int i = 0; i < kPairs; ++i) mbar_init(bar(Lay::PAIR_EMPTY + i), 2 + 1 + 8);  // producers, MMA, softmax warps
+    mbar_init(bar(Lay::ENDING), 2);                                                   // producers
     *reinterpret_cast<volatile int*>(smem + Lay::FLAG_OFF + 4) = 0;
     loaded[0] = loaded[1] = ~0u;
     fence_barrier_init();
@@ -353,6 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = g ? n1 : n0, units = it->units, kvrow = it->kvrow;
         Place<NS> at = place;
         place.advance_any(2 * (n0 + n1));
+        // The next pair is asked for when the loads of this one are kAhead tiles from their end (see warp 3).
+        auto ending = [&](int t) {
+          if (t == max(n - kAhead, 0) && lane == 0) mbar_arrive(bar(Lay::ENDING));
+        };
+        if (n == 0) ending(0);
         if (n > 0) {
           // Q, once the item before is done with its S products
           if (items_done > 0) {
@@ -385,6 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // loads of the round (item 1)
           at.advance(1 + (g == 0 ? (n1 > 0) : (n0 > 0) + (n0 > 1)));
           for (int t = 0; t < n && ok; ++t) {
+            ending(t);
             ok = load(&tmv, at, keys, units - 2 * t > 1, kvrow);
             if (!ok || t + 1 == n) break;
             at.advance(1);
@@ -503,10 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int cta = blockIdx.x;
       bool ok = true;
       for (int k = 0; ok && cta >= 0; ++k) {
-        // the place's pair before this one has been let go by all: no CTA is taken over earlier
-        // than when the pair before it is begun, so the last ones go to whoever is free
-        const bool free_ = mbar_wait_or_abort(bar(Lay::PAIR_EMPTY + k % kPairs), ((k / kPairs) & 1) ^ 1, abort_flag, a.err,
-                                              ERR_WAIT_EPI);
+        // The place's pair before this one has been let go by all, and the pair before this one nears its end:
+        // a CTA is taken over no earlier than its loads need, so the last ones go to whoever is free first.
+        bool free_ = mbar_wait_or_abort(bar(Lay::PAIR_EMPTY + k % kPairs), ((k / kPairs) & 1) ^ 1, abort_flag, a.err,
+                                        ERR_WAIT_EPI);
+        if (k > 0) free_ = free_ && mbar_wait_or_abort(bar(Lay::ENDING), (k - 1) & 1, abort_flag, a.err, ERR_WAIT_EPI);
         ok = __all_sync(0xFFFFFFFFu, free_);
         if (!ok) break;
         if (k > 0) {
