@@ -94,7 +94,7 @@ def test_padded_items_and_garbage_behind_them(dh, block_k):
     check(q, k, v, blocks, counts, block_k, q_lens, kv_lens)
 
 
-@pytest.mark.parametrize("Lq", [300, 3])
+@pytest.mark.parametrize("Lq", [300, 3, 2, 1])
 def test_lists_that_hold_no_key_bad_entries_and_repeats(Lq):
     require_gpu()
     B, H, dh, Lk = 1, 2, 128, 1000
@@ -164,7 +164,7 @@ def test_lists_of_the_selection():
     assert ((o.double() - dense.double()).abs() <= tol).all()
 
 
-@pytest.mark.parametrize("Lq,Lk,topk", [(700, 700, 5), (1, 6000, 60)])
+@pytest.mark.parametrize("Lq,Lk,topk", [(700, 700, 5), (3, 6000, 60), (1, 6000, 60)])
 def test_streams_graphs_and_repeats_are_bit_equal(Lq, Lk, topk):
     require_gpu()
     B, H, KV, dh = 2, 4, 2, 128
@@ -211,7 +211,7 @@ def test_workspace_size_is_enough():
 
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
-@pytest.mark.parametrize("Lq", [200, 1])
+@pytest.mark.parametrize("Lq", [200, 5, 1])
 def test_a_bad_key_reaches_every_query_that_lists_it(value, Lq):
     """A NaN or infinite score makes the formula's row NaN, wherever in its tile the key lies."""
     require_gpu()
@@ -244,3 +244,26 @@ def test_more_pairs_of_query_blocks_than_processors(dh, block_k, kv_lens):
             v[b, :, kv_lens[b]:] = float("nan")
     check(q, k, v, blocks, counts, block_k, None, kv_lens)
     check(q, k, v, blocks[..., :3].contiguous(), None, block_k, [1024, 1000, 1], kv_lens)
+
+
+@pytest.mark.parametrize("Lq", [1, 2, 3, 9])
+@pytest.mark.parametrize("B,H,KV,dh,Lk,block_k,topk", [
+    (4, 40, 8, 128, 3000, 64, 20),
+    (1, 2, 1, 64, 100, 64, 2),
+    (3, 5, 5, 64, 9001, 128, 71),
+    (1, 1, 1, 128, 64 * 600, 64, 600),
+    (300, 1, 1, 128, 130, 64, 3),
+])
+def test_few_queries(Lq, B, H, KV, dh, Lk, block_k, topk):
+    """A few new tokens of each stream over long and short latents, padded items among them."""
+    require_gpu()
+    q, k, v = randn((B, H, Lq, dh), 44), randn((B, KV, Lk, dh), 45), randn((B, KV, Lk, dh), 46)
+    nkb = -(-Lk // block_k)
+    blocks, counts = lists(B, H, 1, nkb, topk, 47)
+    check(q, k, v, blocks, None, block_k)
+    kv_lens = [(Lk - 37 * b) % (Lk + 1) for b in range(B)]
+    q_lens = [Lq - b % 2 for b in range(B)]
+    for b in range(B):
+        k[b, :, kv_lens[b]:] = float("nan")
+        v[b, :, kv_lens[b]:] = float("inf")
+    check(q, k, v, blocks, counts, block_k, q_lens, kv_lens)

@@ -977,7 +977,7 @@ h3b_status h3b_sparse_workspace_size(const h3b_sparse_dims* dims, size_t* bytes)
   if (s != H3B_OK) return s;
   if (!bytes) return fail(H3B_ERR_ARG, "bytes is NULL");
   *bytes = align256(std::max(select_ws_bytes(dims->B, dims->n_heads, dims->n_kv_heads, dims->head_dim, nqb, nkb),
-                             sparse_attn_ws_bytes(dims->B, dims->n_heads, dims->head_dim, nqb, dims->topk,
+                             sparse_attn_ws_bytes(dims->B, dims->n_heads, dims->head_dim, dims->Lq, nqb, dims->topk,
                                                   dims->block_k)));
   return H3B_OK;
 }

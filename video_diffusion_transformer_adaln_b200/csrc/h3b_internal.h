@@ -118,8 +118,11 @@ struct SparseAttnArgs {
   void* ws;
   unsigned* err;
 };
-size_t sparse_attn_ws_bytes(int B, int n_heads, int head_dim, int nqb, int topk, int block_k);
+size_t sparse_attn_ws_bytes(int B, int n_heads, int head_dim, int Lq, int nqb, int topk, int block_k);
 cudaError_t launch_sparse_attention(const SparseAttnArgs& a, cudaStream_t st);
+// The same for one query per head, a.Lq == 1 (k_sparse_rows.cu): rows of K and V through the FP32 pipe.
+size_t sparse_rows_ws_bytes(long long rows, int head_dim, int topk, int block_k);
+cudaError_t launch_sparse_rows(const SparseAttnArgs& a, cudaStream_t st);
 
 // ---- gated residual with norms on both sides (k_resnorm.cu)
 struct ResNormArgs {

@@ -274,14 +274,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t IDESC_S_HALF = instr_desc(1, 1, 0, 0, kSparseQueries, kUnit);
   constexpr uint32_t IDESC_PV = instr_desc(1, 1, 0, 1, kSparseQueries, DH);
 
+  static_assert(Lay::NBARS <= kThreads, "a thread per barrier");
+  if (threadIdx.x < Lay::NBARS) {
+    const int i = threadIdx.x;
+    // arrivals: P of an item by its softmax warps; a pair is let go by producers, MMA and softmax warps
+    const bool p_full = i >= Lay::P_FULL && i < Lay::P_FULL + 2;
+    const bool pair_empty = i >= Lay::PAIR_EMPTY && i < Lay::PAIR_EMPTY + kPairs;
+    mbar_init(bar(i), p_full ? 4 : pair_empty ? 2 + 1 + 8 : i == Lay::ENDING ? 2 : 1);
+    fence_barrier_init();
+  }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < Lay::NBARS; ++i) mbar_init(bar(i), 1);
-    for (int g = 0; g < 2; ++g) mbar_init(bar(Lay::P_FULL + g), 4);                  // softmax warps of an item
-    for (int i = 0; i < kPairs; ++i) mbar_init(bar(Lay::PAIR_EMPTY + i), 2 + 1 + 8);  // producers, MMA, softmax warps
-    mbar_init(bar(Lay::ENDING), 2);                                                   // producers
     *reinterpret_cast<volatile int*>(smem + Lay::FLAG_OFF + 4) = 0;
     loaded[0] = loaded[1] = ~0u;
-    fence_barrier_init();
     tma_prefetch_desc(&tmq);
     tma_prefetch_desc(&tmk);
     tma_prefetch_desc(&tmv);
@@ -872,13 +876,15 @@ cudaError_t launch(const SparseAttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t sparse_attn_ws_bytes(int B, int n_heads, int head_dim, int nqb, int topk, int block_k) {
+size_t sparse_attn_ws_bytes(int B, int n_heads, int head_dim, int Lq, int nqb, int topk, int block_k) {
   const long long rows = (long long)B * n_heads * nqb;
+  if (Lq == 1) return sparse_rows_ws_bytes(rows, head_dim, topk, block_k);
   const Split sp = choose_split(rows, topk, block_k);
   return sp.n > 1 ? (size_t)rows * sp.n * kSparseQueries * (head_dim * 4 + 8) : 0;
 }
 
 cudaError_t launch_sparse_attention(const SparseAttnArgs& a, cudaStream_t st) {
+  if (a.Lq == 1) return launch_sparse_rows(a, st);
   return a.head_dim == 128 ? launch<128>(a, st) : launch<64>(a, st);
 }
 
