@@ -332,14 +332,34 @@ __global__ void __launch_bounds__(128) sparse_rows_join_kernel(const SparseAttnA
   const int c0 = cta_of((long long)row * d.units), c1 = cta_of((long long)(row + 1) * d.units - 1);
   constexpr int V = DH / 32;
   float M = kNoMax, L = 0.0f, o[V] = {};
-  auto part = [&](int c) { return parts + ((long long)c * d.most + row - d.first(c) / d.units) * (DH + 2); };
-  for (int c = c0; c <= c1; ++c) M = max_nan(M, part(c)[DH]);
-  for (int c = c0; c <= c1; ++c) {
-    const float* p = part(c);
-    const float w = fast_exp2(p[DH] - M);
-    L = fmaf(w, p[DH + 1], L);
+  for (int base = c0; base <= c1; base += 32) {  // a part per lane: its place, maximum and sum
+    const int c = base + lane;
+    long long at = 0;
+    float pm = kNoMax, pl = 0.0f;
+    if (c <= c1) {
+      at = ((long long)c * d.most + row - d.first(c) / d.units) * (DH + 2);
+      pm = parts[at + DH];
+      pl = parts[at + DH + 1];
+    }
+    float top = max_nan(M, pm);
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = fmaf(w, p[lane * V + e], o[e]);
+    for (int x = 16; x > 0; x >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+    const float before = fast_exp2(M - top), w = fast_exp2(pm - top);
+    M = top;
+    float sum = w * pl;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+    L = fmaf(L, before, sum);
+#pragma unroll
+    for (int e = 0; e < V; ++e) o[e] *= before;
+    const int n = min(32, c1 - base + 1);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* p = parts + __shfl_sync(0xFFFFFFFFu, at, i);
+      const float f = __shfl_sync(0xFFFFFFFFu, w, i);
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = fmaf(f, p[lane * V + e], o[e]);
+    }
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   float amax = 0.0f;
