@@ -51,6 +51,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kUnitBox = kUnit * 128;  // bytes of 64 rows x 64 lanes
 constexpr int kBox = kTile * 128;      // bytes of 128 rows x 64 lanes
 constexpr int kPairs = 2;              // pairs of items in flight in a CTA
+constexpr int kSms = 148;               // of a B200
 constexpr int kAhead = 3;              // tiles before a pair's end at which the next is asked for
 constexpr int kItemBytes = 64;
 constexpr float kNoMax = -3.0e38f;     // running maximum before any key
@@ -58,8 +59,9 @@ constexpr float kNoMax = -3.0e38f;     // running maximum before any key
 struct SparseParams {
   SparseAttnArgs a;
   int nsplit, split_tiles, rows;  // items = rows * nsplit, item = row * nsplit + split
+  int per_cta;                    // items of a pair: 2, or 1 where there are processors for all items
   float scale_log2;
-  float* part_o;   // [item][128][DH], nsplit > 1
+  float4* part_o;  // [item][DH / 4][128], nsplit > 1: neighbouring rows side by side, as the threads that write them
   float2* part_ml; // [item][128]: maximum (in exponents of 2), sum
 };
 
@@ -514,15 +516,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile int* abort_flag = flag_at(sb);
       int cta = blockIdx.x;
       bool ok = true;
+      const bool more = gridDim.x > kSms;  // else every CTA starts by itself
       for (int k = 0; ok && cta >= 0; ++k) {
         // The place's pair before this one has been let go by all, and the pair before this one nears its end:
         // a CTA is taken over no earlier than its loads need, so the last ones go to whoever is free first.
         bool free_ = mbar_wait_or_abort(bar(Lay::PAIR_EMPTY + k % kPairs), ((k / kPairs) & 1) ^ 1, abort_flag, a.err,
                                         ERR_WAIT_EPI);
-        if (k > 0) free_ = free_ && mbar_wait_or_abort(bar(Lay::ENDING), (k - 1) & 1, abort_flag, a.err, ERR_WAIT_EPI);
+        if (k > 0 && more) free_ = free_ && mbar_wait_or_abort(bar(Lay::ENDING), (k - 1) & 1, abort_flag, a.err, ERR_WAIT_EPI);
         ok = __all_sync(0xFFFFFFFFu, free_);
         if (!ok) break;
-        if (k > 0) {
+        if (k > 0 && !more) {
+          cta = -1;
+        } else if (k > 0) {
           if (lane == 0) {
             fence_proxy_async_smem();  // the response before was read from the same place
             mbar_arrive_expect_tx(bar(Lay::CANCEL), 16);
@@ -539,8 +544,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item it0{}, it1{};
         it0.tiles = -1;
         if (cta >= 0) {
-          it0 = load_item(p, 2 * cta);
-          it1 = load_item(p, 2 * cta + 1);
+          it0 = load_item(p, p.per_cta * cta);
+          if (p.per_cta == 2) it1 = load_item(p, 2 * cta + 1);
         }
         Item* to = static_cast<Item*>(__cvta_shared_to_generic(sb + Lay::ITEM_OFF + (k % kPairs) * 2 * kItemBytes));
         if (lane == 0) {
@@ -724,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int b = it->bh / a.n_heads, h = it->bh - b * a.n_heads;
         const int dm = a.n_heads * DH;
         const long long o_at = ((long long)b * a.Lq + q) * dm + h * DH;
-        const long long part_at = ((long long)item * kSparseQueries + row) * DH;
+        const long long part_at = (long long)item * (DH / 4) * kSparseQueries + row;
         const float inv_l = 1.0f / l_run;
         const float2 il2 = make_float2(inv_l, inv_l);
         float amax = 0.0f;
@@ -735,10 +740,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           tmem_reg_fence(o);
           if (p.nsplit > 1) {
-            if (mine && !empty_row && H3B_IDX_OK(part_at + c * 32 + 31, (long long)p.rows * p.nsplit * kSparseQueries * DH, a.err)) {
-              uint4* d4 = reinterpret_cast<uint4*>(p.part_o + part_at + c * 32);
+            if (mine && !empty_row &&
+                H3B_IDX_OK(part_at + (c * 8 + 7) * kSparseQueries, (long long)p.rows * p.nsplit * (DH / 4) * kSparseQueries, a.err)) {
+              float4* d4 = p.part_o + part_at + c * 8 * kSparseQueries;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) d4[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int e = 0; e < 8; ++e)
+                d4[e * kSparseQueries] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                     __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
             }
           } else {
             uint32_t pk[16];
@@ -778,68 +786,92 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the items of a split list: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s. A warp per query row.
+// Joins the items of a split list: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s. A CTA per 32 query rows and
+// 32 lanes of the head, a thread per row and four lanes. The parts' weights are formed once, in shared memory, so
+// that the loads of the parts wait for nothing; the output is turned into rows in shared memory.
+constexpr int kMaxSplit = 64;
 template <int DH>
-__global__ void __launch_bounds__(128) sparse_join_kernel(const SparseParams p) {
+__global__ void __launch_bounds__(256) sparse_join_kernel(const SparseParams p) {
   griddep_wait();
   griddep_launch_dependents();
+  __shared__ float2 weight[kMaxSplit][32];  // maximum and sum of a part's row; then its weight, and whether it has one
+  __shared__ float tile[32][36];
   const SparseAttnArgs& a = p.a;
-  const int lane = threadIdx.x & 31;
-  const int row_item = blockIdx.x / (kSparseQueries / 4), r = (blockIdx.x % (kSparseQueries / 4)) * 4 + (threadIdx.x >> 5);
-  const int bh = row_item / a.nqb, qb = row_item - bh * a.nqb;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int list = blockIdx.x >> 2, r0 = (blockIdx.x & 3) * 32, r = r0 + lane;
+  const int bh = list / a.nqb, qb = list - bh * a.nqb;
   const int b = bh / a.n_heads, h = bh - b * a.n_heads;
-  const int q = qb * kSparseQueries + r;
-  if (q >= clamp_len(a.q_lens, b, a.Lq)) return;
-  constexpr int V = DH / 32;  // lanes of the head per thread
-  const size_t first = (size_t)row_item * p.nsplit;
-  float M = kNoMax;
-  for (int s = 0; s < p.nsplit; ++s) M = fmaxf(M, p.part_ml[(first + s) * kSparseQueries + r].x);
-  float l = 0.0f, o[V] = {};
-  for (int s = 0; s < p.nsplit; ++s) {
-    const float2 ml = p.part_ml[(first + s) * kSparseQueries + r];
-    if (ml.y == 0.0f) continue;  // no key in this range: its O was not written
-    const float w = fast_exp2(ml.x - M);
-    l = fmaf(w, ml.y, l);
-    const float* src = p.part_o + ((first + s) * kSparseQueries + r) * DH + lane * V;
+  const int valid = clamp_len(a.q_lens, b, a.Lq) - qb * kSparseQueries;  // rows of the query block
+  if (r0 >= valid) return;                                               // block-uniform
+  const size_t first = (size_t)list * p.nsplit;
+  const bool mine = r < valid;
+  const int n = p.nsplit;
+  for (int s = warp; s < n; s += 8)
+    weight[s][lane] = mine ? p.part_ml[(first + s) * kSparseQueries + r] : make_float2(kNoMax, 0.0f);
+  const float4* src = p.part_o + (first * (DH / 4) + 8 * blockIdx.y + warp) * kSparseQueries + r;
+  constexpr size_t step = (size_t)(DH / 4) * kSparseQueries;  // from one part to the next
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v[8];
+  auto fetch = [&](int s0) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = fmaf(w, src[e], o[e]);
+    for (int i = 0; i < 8; ++i) v[i] = mine && s0 + i < n ? src[(s0 + i) * step] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
+  fetch(0);
+  __syncthreads();
+  float M = kNoMax;
+  for (int s = 0; s < n; ++s) M = fmaxf(M, weight[s][lane].x);
+  float l = 0.0f;
+  for (int s0 = 0; s0 < n; s0 += 8) {
+    float4 u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = v[i];
+    fetch(s0 + 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (s0 + i >= n) break;
+      const float2 ml = weight[s0 + i][lane];
+      if (ml.y == 0.0f) continue;  // no key in its range: its output was not written; a NaN sum counts
+      const float w = fast_exp2(ml.x - M);
+      l = fmaf(w, ml.y, l);
+      o = make_float4(fmaf(w, u[i].x, o.x), fmaf(w, u[i].y, o.y), fmaf(w, u[i].z, o.z), fmaf(w, u[i].w, o.w));
+    }
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  float amax = 0.0f;
-  uint32_t pk[V / 2];
+  *reinterpret_cast<float4*>(&tile[lane][4 * warp]) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  __syncthreads();
+  // eight threads per row, four lanes of the head each
+  const int i = threadIdx.x >> 3, c = 4 * (threadIdx.x & 7);
+  const float4 x = *reinterpret_cast<const float4*>(&tile[i][c]);
+  const uint2 pk = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+  float amax = fmaxf(max3f(fabsf(bf16_lo(pk.x)), fabsf(bf16_hi(pk.x)), fabsf(bf16_lo(pk.y))), fabsf(bf16_hi(pk.y)));
 #pragma unroll
-  for (int e = 0; e < V / 2; ++e) {
-    pk[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-    amax = max3f(amax, fabsf(bf16_lo(pk[e])), fabsf(bf16_hi(pk[e])));
-  }
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-  const long long at = ((long long)b * a.Lq + q) * a.n_heads * DH + h * DH + lane * V;
-  if (H3B_IDX_OK(at + V - 1, (long long)a.B * a.Lq * a.n_heads * DH, a.err)) {
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + at);
-#pragma unroll
-    for (int e = 0; e < V / 2; ++e) dst[e] = pk[e];
-  }
-  if (a.absmax && lane == 0) atomicMax(reinterpret_cast<unsigned*>(a.absmax) + (size_t)b * a.Lq + q, __float_as_uint(amax));
+  for (int d = 4; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+  if (r0 + i >= valid) return;
+  const int q = qb * kSparseQueries + r0 + i;
+  const long long at = ((long long)b * a.Lq + q) * a.n_heads * DH + h * DH + 32 * blockIdx.y + c;
+  if (H3B_IDX_OK(at + 3, (long long)a.B * a.Lq * a.n_heads * DH, a.err))
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + at) = pk;
+  if (a.absmax && c == 0) atomicMax(reinterpret_cast<unsigned*>(a.absmax) + (size_t)b * a.Lq + q, __float_as_uint(amax));
 }
 
-// Items per list. A CTA works on two items at a time, and its start and end cost
-// about as much as three tiles; the rule takes the split with the fewest tile
-// times over all waves. 148 SMs, whatever the device has: the workspace's size
-// must not depend on the device.
+// Items per list. In units of a tile of a CTA with one item (1.77 us): a tile of two items at once takes 1.2, an
+// item's start and end 1.3 in each round of CTAs; joining 2.5, and for each part 0.02 with 128 query rows. The rule
+// takes the split with the least time. 148 SMs, whatever the device has: the workspace's size must not depend on
+// the device. Measured with 100 queries over 36 tiles: 8 lists in one part each 73 us, as the rule splits them
+// 16 us; 40 lists 75 and 28 us, 160 lists 91 and 83 us.
 struct Split {
   int n, tiles;  // items per list, tiles per item
 };
-Split choose_split(long long rows, int topk, int block_k) {
+Split choose_split(long long rows, int Lq, int topk, int block_k) {
   const int tiles = (topk * (block_k / kUnit) + 1) / 2;
   Split best{1, tiles};
-  long long best_cost = -1;
-  for (int n = 1; n <= 64 && n <= tiles; ++n) {
+  double best_cost = -1.0;
+  for (int n = 1; n <= kMaxSplit && n <= tiles; ++n) {
     const int per = (tiles + n - 1) / n, used = (tiles + per - 1) / per;
-    const long long waves = ((rows * used + 1) / 2 + 147) / 148;
-    const long long cost = waves * (per + 3) + (used > 1 ? 3 : 0);
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
+    const long long items = rows * used;
+    const double rounds = items <= kSms ? (double)per : (double)(((items + 1) / 2 + kSms - 1) / kSms) * (1.2 * per + 1.3);
+    const double joined = used > 1 ? 2.5 + 0.02 * (double)items * std::min(Lq, kSparseQueries) / kSparseQueries : 0.0;
+    if (best_cost < 0 || rounds + joined < best_cost) {
+      best_cost = rounds + joined;
       best = {used, per};
     }
   }
@@ -852,14 +884,15 @@ cudaError_t launch(const SparseAttnArgs& a, cudaStream_t st) {
   SparseParams p{};
   p.a = a;
   p.rows = a.B * a.n_heads * a.nqb;
-  const Split sp = choose_split(p.rows, a.topk, a.block_k);
+  const Split sp = choose_split(p.rows, a.Lq, a.topk, a.block_k);
   p.nsplit = sp.n;
   p.split_tiles = sp.tiles;
   p.scale_log2 = 1.4426950408889634f / sqrtf((float)DH);
   const size_t items = (size_t)p.rows * p.nsplit;
+  p.per_cta = items <= kSms ? 1 : 2;
   if (p.nsplit > 1) {
-    p.part_o = static_cast<float*>(a.ws);
-    p.part_ml = reinterpret_cast<float2*>(p.part_o + items * kSparseQueries * DH);
+    p.part_o = static_cast<float4*>(a.ws);
+    p.part_ml = reinterpret_cast<float2*>(p.part_o + items * kSparseQueries * (DH / 4));
   }
   CUtensorMap tmq, tmk, tmv;
   if (!make_tmap_3d(&tmq, a.q, 2, DH, a.Lq, (uint64_t)a.B * a.n_heads, 64, kSparseQueries) ||
@@ -869,9 +902,9 @@ cudaError_t launch(const SparseAttnArgs& a, cudaStream_t st) {
   auto k = sparse_attention_kernel<DH, 4>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::SMEM);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k, dim3((unsigned)((items + 1) / 2)), dim3(kThreads), Lay::SMEM, st, tmq, tmk, tmv, p);
+  e = launch_pdl(k, dim3((unsigned)((items + p.per_cta - 1) / p.per_cta)), dim3(kThreads), Lay::SMEM, st, tmq, tmk, tmv, p);
   if (e != cudaSuccess || p.nsplit == 1) return e;
-  return launch_pdl(sparse_join_kernel<DH>, dim3(p.rows * (kSparseQueries / 4)), dim3(128), 0, st, p);
+  return launch_pdl(sparse_join_kernel<DH>, dim3(p.rows * (kSparseQueries / 32), DH / 32), dim3(256), 0, st, p);
 }
 
 }  // namespace
@@ -879,7 +912,7 @@ cudaError_t launch(const SparseAttnArgs& a, cudaStream_t st) {
 size_t sparse_attn_ws_bytes(int B, int n_heads, int head_dim, int Lq, int nqb, int topk, int block_k) {
   const long long rows = (long long)B * n_heads * nqb;
   if (Lq == 1) return sparse_rows_ws_bytes(rows, head_dim, topk, block_k);
-  const Split sp = choose_split(rows, topk, block_k);
+  const Split sp = choose_split(rows, Lq, topk, block_k);
   return sp.n > 1 ? (size_t)rows * sp.n * kSparseQueries * (head_dim * 4 + 8) : 0;
 }
 
