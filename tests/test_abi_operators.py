@@ -199,3 +199,12 @@ def test_structs_have_the_header_layout():
     assert C.sizeof(h3b.QkDims) == 48 and h3b.QkDims.row_stride.offset == 40 and h3b.QkDims.rope_theta.offset == 32
     assert C.sizeof(h3b.SparseDims) == 40 and h3b.SparseDims.keep_local.offset == 36
     assert C.sizeof(h3b.ResidualNormDims) == 36 and h3b.ResidualNormDims.post_eps.offset == 24
+
+
+def test_grid_positions():
+    from video_diffusion_transformer_adaln_b200.runtime import grid_positions
+    d = h3b.make_dims(2, 2, 3, 4, 256, 4, 64, 256, (16, 24, 24))
+    pos = grid_positions(d, offset=(10.0, 0.0, 0.5), step=(0.5, 1.0, 2.0), device="cpu")
+    assert pos.shape == (2, 24, 3) and pos.dtype == torch.float32 and pos.is_contiguous()
+    for l in range(24):
+        assert pos[1, l].tolist() == [10.0 + 0.5 * (l // 12), float(l // 4 % 3), 0.5 + 2.0 * (l % 4)]

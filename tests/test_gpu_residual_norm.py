@@ -87,12 +87,21 @@ def test_rows_and_items(rows, rpi):
     check(rows, 256, "rms", "layer", rpi, in_place=True)
 
 
+@pytest.mark.parametrize("rows,d,rpi", [(9600, 256, 2400), (9500, 264, 9500), (2500, 5120, 833), (5000, 2056, 2500),
+                                        (1300, 8192, 1300)])
+def test_many_rows_share_an_item(rows, d, rpi):
+    """The item's vectors folded in shared memory; items end inside a pass."""
+    require_gpu()
+    check(rows, d, "rms", "layer", rpi, alpha=0.7, in_place=True)
+
+
 @pytest.mark.parametrize("weight,gated,modulated", [(False, True, True), (True, False, True), (True, True, False),
                                                     (False, False, False)])
 def test_optional_vectors(weight, gated, modulated):
     require_gpu()
     check(29, 768, "rms", "rms", 10, weight=weight, gated=gated, modulated=modulated)
     check(29, 5120, "layer", "layer", 29, weight=weight, gated=gated, modulated=modulated)
+    check(9600, 128, "layer", "rms", 4800, weight=weight, gated=gated, modulated=modulated)
 
 
 def test_rows_without_spread_and_zero_rows():

@@ -112,3 +112,77 @@ def paired_block_forward(full: h3b.Dims, merged: h3b.Dims, blk: DeviceBlock, c: 
     h3b.h3b_block_forward(merged, blk.struct, c, ym, ws)
     h3b.h3b_token_unpair(full, x, None, ym, x)
     return ym
+
+
+def grid_positions(wl_or_dims, offset=(0.0, 0.0, 0.0), step=(1.0, 1.0, 1.0), device="cuda") -> torch.Tensor:
+    """fp32 [B][L][3] (t, h, w) positions of a latent grid's tokens for h3b_qk_norm_rope: offset + step * index
+    along each axis (a clip that starts late, a frame rate, the midpoints of merged tokens)."""
+    d = wl_or_dims
+    axes = [o + s * torch.arange(n, dtype=torch.float32, device=device)
+            for n, o, s in zip((d.T, d.H, d.W), offset, step)]
+    grid = torch.stack(torch.meshgrid(*axes, indexing="ij"), -1).reshape(1, d.T * d.H * d.W, 3)
+    return grid.expand(d.B, -1, -1).contiguous()
+
+
+class SparseBlockState:
+    """Buffers and plans of sparse_block_forward for one grid, kept between calls. Calls that may run at the same
+    time need a state each.
+
+    topk of the key blocks of block_k tokens are attended by each block of 128 queries; keep_first and keep_local
+    as in h3b_select_blocks."""
+
+    def __init__(self, dims: h3b.Dims, block_k: int = 64, topk: int = 1, keep_first: int = 0, keep_local: int = 0,
+                 norm_eps: float = 1e-6, device="cuda"):
+        if not dims.qkv_int8 or dims.wo_bf16:
+            raise ValueError("sparse_block_forward takes int8 projections (qkv_int8 = 1, wo_bf16 = 0)")
+        B, L, d, F, H, dh = dims.B, dims.L, dims.d, dims.d_ff, dims.n_heads, dims.head_dim
+        R = B * L
+        e = lambda *s, dtype=torch.bfloat16: torch.empty(s, dtype=dtype, device=device)  # noqa: E731
+        self.dims = dims
+        self.qk = h3b.make_qk(B, L, H, H, dh, (dims.rope_t, dims.rope_h, dims.rope_w), dims.rope_theta, norm_eps)
+        self.sparse = h3b.make_sparse(B, H, H, dh, L, L, block_k, topk, keep_first, keep_local)
+        # after attention: the next branch's LayerNorm and quantizer; after the MLP: the residual alone
+        self.after = h3b.make_residual_norm(R, d, L, 6 * d, "rms", "layer", norm_eps, dims.ln_eps)
+        self.mod = e(B, 6 * d, dtype=torch.float32)
+        self.codes, self.scales = e(R * max(d, F), dtype=torch.int8), e(R, dtype=torch.float32)
+        self.absmax = e(R, dtype=torch.float32)
+        self.proj = e(R, 3 * d)        # Q | K | V of the projection, then the branches' outputs
+        self.hidden = e(R, F)
+        self.q, self.k, self.v, self.o = e(B, H, L, dh), e(B, H, L, dh), e(B, H, L, dh), e(B, L, d)
+        nqb = self.sparse.nqb
+        self.blocks, self.counts = e(B, H, nqb, topk, dtype=torch.int32), e(B, H, nqb, dtype=torch.int32)
+        self.ws = e(h3b.h3b_sparse_workspace_size(self.sparse), dtype=torch.uint8)
+
+
+def sparse_block_forward(state: SparseBlockState, blk: DeviceBlock, norms: Dict[str, torch.Tensor], c: torch.Tensor,
+                         x: torch.Tensor, pos: torch.Tensor):
+    """One block in place on x (bf16 [B][L][d]) with attention over selected key blocks, per-head norms of Q and K
+    at the tokens' positions `pos` (fp32 [B][L][3]), and an RMSNorm of each branch's output ahead of its gate:
+
+      A1 = quant(LN(x)(1 + scale_attn) + shift_attn);  Q, K, V = A1 Wqkv^T, Q and K normalised and rotated
+      O = softmax over the listed key blocks;          x += gate_attn * (RMS(quant(O) Wo^T) * post_attn)
+      A3 = quant(LN(x)(1 + scale_mlp) + shift_mlp);    x += gate_mlp * (RMS(quant(GELU(A3 W1^T)) W2^T) * post_mlp)
+
+    norms: fp32 vectors "q", "k" [head_dim] and "post_attn", "post_mlp" [d] (missing ones: see h3b_qk_norm_rope and
+    h3b_residual_norm). The listed blocks stay in state.blocks and state.counts."""
+    s, dims, t = state, state.dims, blk.tensors
+    d, F, R = dims.d, dims.d_ff, dims.B * dims.L
+    shift_a, scale_a, gate_a, shift_m, scale_m, gate_m = (s.mod[:, i * d:(i + 1) * d] for i in range(6))
+    a_d, a_f = s.codes[:R * d].view(R, d), s.codes[:R * F].view(R, F)
+    y = s.proj.view(-1)[:R * d].view(R, d)
+    xf = x.view(R, d)
+    h3b.h3b_adaln_modulation(dims, t["w_ada"], t.get("b_ada"), c, s.mod)
+    h3b.h3b_ln_modulate_quantize(xf, R, d, dims.ln_eps, shift_a, scale_a, dims.L, 6 * d, a_d, s.scales,
+                                 absmax_zero=s.absmax)
+    h3b.h3b_gemm_i8_dequant(a_d, s.scales, t["wqkv"], t["sqkv"], t.get("bqkv"), s.proj)
+    h3b.h3b_qk_norm_rope(s.qk, s.proj, norms.get("q"), norms.get("k"), pos, s.q, s.k, s.v)
+    h3b.h3b_select_blocks(s.sparse, s.q, s.k, None, None, s.blocks, s.counts, s.ws)
+    h3b.h3b_attention_blocks(s.sparse, s.q, s.k, s.v, None, None, s.blocks, s.counts, s.o, s.absmax, s.ws)
+    h3b.h3b_quantize_rows(s.o.view(R, d), a_d, s.scales, absmax=s.absmax)
+    h3b.h3b_gemm_i8_dequant(a_d, s.scales, t["wo"], t["so"], t.get("bo"), y)
+    h3b.h3b_residual_norm(s.after, y, norms.get("post_attn"), gate_a, xf, xf, shift_m, scale_m, q=a_d, s=s.scales,
+                          absmax_zero=s.absmax)
+    h3b.h3b_gemm_i8_gelu(a_d, s.scales, t["w1"], t["s1"], t.get("b1"), s.hidden, s.absmax)
+    h3b.h3b_quantize_rows(s.hidden, a_f, s.scales, absmax=s.absmax)
+    h3b.h3b_gemm_i8_dequant(a_f, s.scales, t["w2"], t["s2"], t.get("b2"), y)
+    h3b.h3b_residual_norm(s.after, y, norms.get("post_mlp"), gate_m, xf, xf, None, None)
