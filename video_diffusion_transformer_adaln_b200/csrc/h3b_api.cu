@@ -404,6 +404,20 @@ bool make_tmap_3d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t d
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool set_tmap_address(CUtensorMap* map, const void* base) {
+  typedef CUresult (*ReplaceAddressFn)(CUtensorMap*, void*);
+  static ReplaceAddressFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapReplaceAddress", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<ReplaceAddressFn>(p);
+  });
+  return fn && fn(map, const_cast<void*>(base)) == CUDA_SUCCESS;
+}
+
 bool make_tmap_4d_bf16(CUtensorMap* map, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
                        const uint32_t (&box)[4]) {
   EncodeTiledFn fn = encode_fn();

@@ -155,6 +155,8 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t c
 // 3D tensor [d2][d1][d0] (d0 innermost), box of box0 x box1 x 1, 128-byte swizzle.
 bool make_tmap_3d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t d0, uint64_t d1,
                   uint64_t d2, uint32_t box0, uint32_t box1);
+// The same tensor map for another tensor of that shape.
+bool set_tmap_address(CUtensorMap* map, const void* base);
 // 4D bf16 tensor, dims[0] innermost (contiguous), the other strides in bytes; box without swizzle.
 bool make_tmap_4d_bf16(CUtensorMap* map, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
                        const uint32_t (&box)[4]);

@@ -896,9 +896,10 @@ cudaError_t launch(const SparseAttnArgs& a, cudaStream_t st) {
   }
   CUtensorMap tmq, tmk, tmv;
   if (!make_tmap_3d(&tmq, a.q, 2, DH, a.Lq, (uint64_t)a.B * a.n_heads, 64, kSparseQueries) ||
-      !make_tmap_3d(&tmk, a.k, 2, DH, a.Lk, (uint64_t)a.B * a.n_kv_heads, 64, kUnit) ||
-      !make_tmap_3d(&tmv, a.v, 2, DH, a.Lk, (uint64_t)a.B * a.n_kv_heads, 64, kUnit))
+      !make_tmap_3d(&tmk, a.k, 2, DH, a.Lk, (uint64_t)a.B * a.n_kv_heads, 64, kUnit))
     return cudaErrorInvalidValue;
+  tmv = tmk;  // of the same shape: encoding a third map costs the host a microsecond
+  if (!set_tmap_address(&tmv, a.v)) return cudaErrorInvalidValue;
   auto k = sparse_attention_kernel<DH, 4>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::SMEM);
   if (e != cudaSuccess) return e;
