@@ -256,8 +256,7 @@ cudaError_t launch(const ResNormArgs& a, int tpr, int rpp, int sms, cudaStream_t
   if (e != cudaSuccess) return e;
   const long long rpi = kStaged ? a.rows_per_item : a.rows;
   const long long passes = (a.rows + rpi - 1) / rpi * ((rpi + rpp - 1) / rpp);
-  const int per_sm = smem + 1024 <= 113 * 1024 && rpp * tpr <= 256 ? 2 : 1;
-  return launch_pdl(k, dim3((unsigned)std::min<long long>(passes, (long long)per_sm * sms)), dim3(rpp * tpr), smem, st, a, tpr);
+  return launch_pdl(k, dim3((unsigned)std::min<long long>(passes, sms)), dim3(rpp * tpr), smem, st, a, tpr);
 }
 
 template <int VPT>
