@@ -150,3 +150,25 @@ def test_many_key_blocks():
     require_gpu()
     check(field(1, 1, 700, 64, 18), field(1, 1, 64 * 1537, 64, 19), 64, 100, local=1)
     check(field(1, 2, 130, 128, 20), field(1, 1, 64 * 1536, 128, 21), 64, 9)
+
+
+@pytest.mark.parametrize("other", [0.5, 0.25, 2.0 ** -9, 2.0 ** -60, 0.0, -1.0])
+@pytest.mark.parametrize("topk", [1, 7, 30, 59])
+def test_scores_units_in_the_last_place_apart(other, topk):
+    """Scores 1 + c 2^-52, exact in 64 bits, are told apart whatever the spread of all scores is."""
+    require_gpu()
+    nkb = 60
+    q, k = (torch.zeros((1, 1, n, 64), dtype=torch.bfloat16, device="cuda") for n in (128, 64 * nkb))
+    q[..., 0], q[..., 1] = 1.0, 2.0 ** -52
+    c = torch.randperm(nkb, generator=torch.Generator().manual_seed(topk)) * 4
+    k[..., 0] = 1.0
+    k[..., 1] = c.repeat_interleave(64).to(device="cuda", dtype=torch.bfloat16)
+    k[:, :, 64 * 31:64 * 32, 0] = other
+    check(q, k, 64, topk)
+
+
+@pytest.mark.parametrize("H,KV,Lq,Lk,q_lens,kv_lens", [
+    (6, 2, 300, 1300, None, None), (4, 1, 1300, 300, None, None), (2, 2, 900, 900, [900, 200], [130, 900])])
+def test_kept_blocks_of_shared_heads_and_unequal_lengths(H, KV, Lq, Lk, q_lens, kv_lens):
+    require_gpu()
+    check(field(2, H, Lq, 128, 22), field(2, KV, Lk, 128, 23), 64, 5, q_lens, kv_lens, first=1, local=2)

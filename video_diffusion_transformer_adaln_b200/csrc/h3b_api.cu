@@ -1025,7 +1025,7 @@ h3b_status h3b_select_blocks(const h3b_sparse_dims* dims, const void* q, const v
   if ((s = device_info(&di)) != H3B_OK) return s;
   SelectArgs a{dims->B, dims->n_heads, dims->n_kv_heads, dims->head_dim, dims->Lq, dims->Lk, dims->block_k, dims->topk,
                dims->keep_first, dims->keep_local, nqb, nkb, q, k, q_lens, kv_lens, blocks, counts, ws, di->err};
-  H3B_CK(launch_select_blocks(a, di->sms, st), "select_blocks");
+  H3B_CK(launch_select_blocks(a, st), "select_blocks");
   return H3B_OK;
 }
 

@@ -106,7 +106,7 @@ struct SelectArgs {
   unsigned* err;
 };
 size_t select_ws_bytes(int B, int n_heads, int n_kv_heads, int head_dim, int nqb, int nkb);
-cudaError_t launch_select_blocks(const SelectArgs& a, int sms, cudaStream_t st);
+cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t st);
 
 struct SparseAttnArgs {
   int B, n_heads, n_kv_heads, head_dim, Lq, Lk, block_k, topk;

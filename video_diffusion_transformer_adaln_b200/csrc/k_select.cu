@@ -237,13 +237,14 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
         unsigned long long lo = (unsigned long long)bottom << 32;
         // the range is a power of two above (top - bottom + 1) 2^32, 256 bins of 2^sh
         int sh = max(0, 64 - __clzll((long long)(((unsigned long long)(top - bottom) << 32) | 0xFFFFFFFFull)) - 8);
+        unsigned long long range = 256;  // bins that the range has; fewer once a bin is less than 256 keys wide
         unsigned* bins = hist[warp];
         for (;;) {
           for (int x = lane; x < 64; x += 32) reinterpret_cast<uint4*>(bins)[x] = make_uint4(0, 0, 0, 0);
           __syncwarp();
           for (int j = lane; j < n; j += 32) {
             const unsigned long long v = key[j], d = v - lo;
-            if (v != kKeyKeep && v >= lo && (d >> sh) < 256ull) atomicAdd(bins + (unsigned)(d >> sh), 1u);
+            if (v != kKeyKeep && v >= lo && (d >> sh) < range) atomicAdd(bins + (unsigned)(d >> sh), 1u);
           }
           __syncwarp();
           // this lane's eight bins, and the keys in bins above them
@@ -285,6 +286,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
             break;
           }
           lo = T;
+          range = 1ull << min(sh, 8);
           sh = max(0, sh - 8);
         }
         if (ties == n) T -= 1;  // keys >= T, as keys above T - 1 (T > 0: no key is zero)
@@ -337,8 +339,7 @@ size_t select_ws_bytes(int B, int n_heads, int n_kv_heads, int head_dim, int nqb
   return sizeof(double) * (size_t)(m.nq + m.nk);
 }
 
-cudaError_t launch_select_blocks(const SelectArgs& a, int sms, cudaStream_t st) {
-  (void)sms;
+cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t st) {
   return a.head_dim == 128 ? launch<128>(a, st) : launch<64>(a, st);
 }
 
