@@ -181,3 +181,10 @@ def test_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("rpi", [65, 10 ** 6, 2 ** 31 - 1])
+@pytest.mark.parametrize("rows,d", [(64, 256), (5, 5120), (1, 8)])
+def test_items_longer_than_the_rows(rows, d, rpi):
+    require_gpu()
+    check(rows, d, "rms", "layer", rpi)

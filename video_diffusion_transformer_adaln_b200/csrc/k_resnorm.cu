@@ -116,8 +116,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_kernel(const Res
 
   // passes of rpp rows; staged: of one item each
   const int rpi = kStaged ? a.rows_per_item : a.rows;
-  const unsigned per_item = (unsigned)((rpi + rpp - 1) / rpp);
-  const unsigned items = (unsigned)((a.rows + rpi - 1) / rpi);
+  const unsigned per_item = ((unsigned)rpi + (unsigned)rpp - 1) / (unsigned)rpp;
+  const unsigned items = ((unsigned)a.rows + (unsigned)rpi - 1) / (unsigned)rpi;  // rpi <= rows
   const unsigned passes = items * per_item;  // at most rows, so 32 bits suffice
   unsigned item = blockIdx.x / per_item, in = blockIdx.x % per_item;
   auto row_of = [&](unsigned it, unsigned p) { return (long long)it * rpi + (long long)p * rpp + sub; };
@@ -271,7 +271,9 @@ cudaError_t launch_vpt(const ResNormArgs& a, int tpr, int sms, cudaStream_t st) 
 
 }  // namespace
 
-cudaError_t launch_residual_norm(const ResNormArgs& a, int sms, cudaStream_t st) {
+cudaError_t launch_residual_norm(const ResNormArgs& args, int sms, cudaStream_t st) {
+  ResNormArgs a = args;
+  a.rows_per_item = std::min(a.rows_per_item, a.rows);  // the passes are counted by it
   // Vectors per thread, and as many warps as the row then needs. A warp's way through a row costs about as much
   // as three vectors besides its own, and the row's barriers the more the more warps it has. At 20000 rows of 3080
   // channels: 5 vectors, 3 warps 103 us; 1 vector, 13 warps, with fewer idle lanes, 257 us. At 8000 rows of 8192:
