@@ -499,7 +499,8 @@ H3B_API h3b_status h3b_select_blocks(const h3b_sparse_dims* dims, const void* q,
  * keys of its block's listed key blocks:
  *   o bf16 [B][Lq][n_heads*head_dim]; rows behind q_lens are left as they were.
  *   absmax fp32 [B*Lq] or NULL: each row's max |o| is max-combined into it
- *   (zero it first; rows behind q_lens are left as they were).
+ *   (zero it first; rows behind q_lens are left as they were); a NaN among them
+ *   makes it NaN.
  * A query whose list holds no valid key gets o = 0. counts NULL: every list has
  * topk entries; a count is clamped to [0, topk]. An entry outside [0, nkb) holds
  * no key; a block listed twice counts its keys twice. */
@@ -513,6 +514,8 @@ H3B_API h3b_status h3b_attention_blocks(const h3b_sparse_dims* dims, const void*
  *   x_out = bf16(x + alpha * gate * (post_norm(y) * w_post))
  *   h     = bf16(pre_norm(x_out) * (1 + scale) + shift)
  *   h_out = h, and q, s = the per-row int8 quantizer of h (as h3b_quantize_rows)
+ * a row with a NaN or an infinity gets a NaN or infinite s, so that its products
+ *   do not pass for finite ones, and codes without a meaning.
  * y, x, x_out, h_out bf16 [rows][d]; q int8 [rows][d]; s fp32 [rows].
  * post_norm, pre_norm: 0 none, 1 RMS (x * rsqrt(mean(x^2) + eps)), 2 LayerNorm
  * (no affine, biased variance). x_out may be x; otherwise no output may overlap

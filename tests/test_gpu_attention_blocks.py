@@ -267,3 +267,20 @@ def test_few_queries(Lq, B, H, KV, dh, Lk, block_k, topk):
         k[b, :, kv_lens[b]:] = float("nan")
         v[b, :, kv_lens[b]:] = float("inf")
     check(q, k, v, blocks, counts, block_k, q_lens, kv_lens)
+
+
+@pytest.mark.parametrize("Lq", [200, 5, 1])
+@pytest.mark.parametrize("lane", [0, 63, 127])
+def test_absmax_of_a_row_with_a_nan(Lq, lane):
+    """One lane of a value is NaN: the rows that list it have a NaN there and as their largest magnitude."""
+    require_gpu()
+    B, H, dh, Lk = 2, 2, 128, 3000
+    nqb, nkb = -(-Lq // 128), 47
+    q, k, v = randn((B, H, Lq, dh), 48), randn((B, H, Lk, dh), 49), randn((B, H, Lk, dh), 50)
+    blocks, _ = lists(B, H, nqb, nkb, 20, 51)
+    v[0, 1, 64 * int(blocks[0, 1, 0, 9]) + 3, lane] = float("nan")
+    o, am, _ = run(q, k, v, blocks, None, 64)
+    rows = o.view(B * Lq, -1).isnan().any(-1)
+    assert rows[0] and not rows[Lq:].any()
+    assert torch.equal(am.isnan(), rows)
+    assert torch.equal(am[~rows], o.view(B * Lq, -1)[~rows].abs().amax(-1).float())

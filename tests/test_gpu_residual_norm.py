@@ -188,3 +188,21 @@ def test_on_another_stream_and_in_a_graph():
 def test_items_longer_than_the_rows(rows, d, rpi):
     require_gpu()
     check(rows, d, "rms", "layer", rpi)
+
+
+def test_non_finite_rows_have_non_finite_scales():
+    require_gpu()
+    rows, d = 24, 528
+    y, x, w, mod = make(rows, d, 1, 7)
+    x[3, 5], x[7, 9], y[11, 0] = float("nan"), float("inf"), float("-inf")
+    x[15, 500], x[15, 7] = float("nan"), float("inf")
+    for pre in ("none", "layer"):
+        dims = h3b.make_residual_norm(rows, d, rows, 3 * d, "rms", pre)
+        x_out, h = torch.empty_like(x), torch.empty_like(x)
+        q, s = torch.empty((rows, d), dtype=torch.int8, device="cuda"), torch.empty(rows, device="cuda")
+        h3b.h3b_residual_norm(dims, y, w, mod[:, 0], x, x_out, mod[:, 1], mod[:, 2], h_out=h, q=q, s=s)
+        assert torch.equal(s.isnan(), h.isnan().any(-1)) and torch.equal(s.isfinite(), h.isfinite().all(-1))
+        ok = h.isfinite().all(-1)
+        assert int(ok.sum()) == rows - 4
+        qr, sr = R.quantized(h[ok])
+        assert torch.equal(q[ok], qr) and torch.equal(s[ok], sr)

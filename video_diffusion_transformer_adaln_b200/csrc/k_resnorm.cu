@@ -66,12 +66,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_kernel(const Res
     return v;
   };
   auto row_max = [&](float v) {
-    v = warp_max(v);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
     if (wpr == 1) return v;
     if (lane == 0) red[slot][warp] = v;
     row_barrier(1 + sub, tpr);
     v = 0.0f;
-    for (int w = 0; w < wpr; ++w) v = fmaxf(v, red[slot][w0 + w]);
+    for (int w = 0; w < wpr; ++w) v = max_nan(v, red[slot][w0 + w]);
     slot ^= 1;
     return v;
   };
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_kernel(const Res
           const int e = 4 * i + 2 * k;
           const float2 p = __ffma2_rn(x[e], make_float2(sc.x, sc.y), make_float2(sh.x, sh.y));
           const float2 q = __ffma2_rn(x[e + 1], make_float2(sc.z, sc.w), make_float2(sh.z, sh.w));
-          am = fmaxf(am, fmaxf(fmaxf(fabsf(p.x), fabsf(p.y)), fmaxf(fabsf(q.x), fabsf(q.y))));
+          am = max3_nan(max3_nan(am, fabsf(p.x), fabsf(p.y)), fabsf(q.x), fabsf(q.y));
           u[2 * k] = pack_bf16x2(p.x, p.y);
           u[2 * k + 1] = pack_bf16x2(q.x, q.y);
         }

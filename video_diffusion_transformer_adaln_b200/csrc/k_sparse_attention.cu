@@ -87,12 +87,6 @@ struct Layout {
 static_assert(Layout<128>::SMEM <= 232448 && Layout<64>::SMEM <= 232448, "shared memory of one CTA");
 static_assert(Layout<64>::SMEM > 116 * 1024, "one CTA per SM: each holds all tensor memory columns");
 
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 __device__ __forceinline__ int clamp_len(const int* lens, int b, int L) {
   return lens ? min(max(__ldg(lens + b), 0), L) : L;
 }
@@ -754,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 16; ++e) {
               const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), il2);
               pk[e] = empty_row ? 0u : pack_bf16x2(v.x, v.y);
-              amax = max3f(amax, fabsf(bf16_lo(pk[e])), fabsf(bf16_hi(pk[e])));
+              amax = max3_nan(amax, fabsf(bf16_lo(pk[e])), fabsf(bf16_hi(pk[e])));
             }
             if (mine && H3B_IDX_OK(o_at + c * 32 + 31, (long long)a.B * a.Lq * dm, a.err)) {
               uint4* d4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + o_at + c * 32);
@@ -842,9 +836,9 @@ __global__ void __launch_bounds__(256) sparse_join_kernel(const SparseParams p) 
   const int i = threadIdx.x >> 3, c = 4 * (threadIdx.x & 7);
   const float4 x = *reinterpret_cast<const float4*>(&tile[i][c]);
   const uint2 pk = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-  float amax = fmaxf(max3f(fabsf(bf16_lo(pk.x)), fabsf(bf16_hi(pk.x)), fabsf(bf16_lo(pk.y))), fabsf(bf16_hi(pk.y)));
+  float amax = max_nan(max3_nan(fabsf(bf16_lo(pk.x)), fabsf(bf16_hi(pk.x)), fabsf(bf16_lo(pk.y))), fabsf(bf16_hi(pk.y)));
 #pragma unroll
-  for (int d = 4; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
+  for (int d = 4; d > 0; d >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
   if (r0 + i >= valid) return;
   const int q = qb * kSparseQueries + r0 + i;
   const long long at = ((long long)b * a.Lq + q) * a.n_heads * DH + h * DH + 32 * blockIdx.y + c;

@@ -33,11 +33,6 @@ constexpr float kNoMax = -3.0e38f;  // running maximum before any key
 __device__ __forceinline__ int clamp_len(const int* lens, int b, int L) {
   return lens ? min(max(__ldg(lens + b), 0), L) : L;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 __device__ __forceinline__ void copy_bytes(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(bar)
@@ -367,10 +362,10 @@ __global__ void __launch_bounds__(128) sparse_rows_join_kernel(const SparseAttnA
 #pragma unroll
   for (int e = 0; e < V / 2; ++e) {
     pk[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-    amax = max3f(amax, fabsf(bf16_lo(pk[e])), fabsf(bf16_hi(pk[e])));
+    amax = max3_nan(amax, fabsf(bf16_lo(pk[e])), fabsf(bf16_hi(pk[e])));
   }
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, x));
+  for (int x = 16; x > 0; x >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, x));
   const long long at = (long long)row * DH + lane * V;
   if (H3B_IDX_OK(at + V - 1, (long long)a.B * a.n_heads * DH, a.err)) {
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(a.o) + at);
