@@ -208,3 +208,21 @@ def test_grid_positions():
     assert pos.shape == (2, 24, 3) and pos.dtype == torch.float32 and pos.is_contiguous()
     for l in range(24):
         assert pos[1, l].tolist() == [10.0 + 0.5 * (l // 12), float(l // 4 % 3), 0.5 + 2.0 * (l % 4)]
+
+
+@pytest.mark.parametrize("bad", [
+    dict(pos=torch.zeros(1, 8, 3)),                             # of one item where the grid has two
+    dict(pos=torch.zeros(1, 8, 3).expand(2, -1, -1)),           # not laid out
+    dict(pos=torch.zeros(2, 8, 3, dtype=torch.float64)),
+    dict(x=torch.zeros(2, 8, 256)),                             # fp32
+    dict(x=torch.zeros(2, 8, 512, dtype=torch.bfloat16)[..., :256]),
+    dict(c=torch.zeros(1, 256)),
+])
+def test_sparse_block_refuses_tensors_that_do_not_fit(L, bad):
+    from types import SimpleNamespace
+    from video_diffusion_transformer_adaln_b200.runtime import SparseBlockState, sparse_block_forward
+    dims = h3b.make_dims(2, 1, 2, 4, 256, 4, 64, 512, (16, 24, 24))
+    state = SparseBlockState(dims, device="cpu")
+    good = dict(c=torch.zeros(2, 256), x=torch.zeros(2, 8, 256, dtype=torch.bfloat16), pos=torch.zeros(2, 8, 3))
+    with pytest.raises(ValueError, match=next(iter(bad))):
+        sparse_block_forward(state, SimpleNamespace(tensors={}), {}, **{**good, **bad})

@@ -167,6 +167,10 @@ def sparse_block_forward(state: SparseBlockState, blk: DeviceBlock, norms: Dict[
     h3b_residual_norm). The listed blocks stay in state.blocks and state.counts."""
     s, dims, t = state, state.dims, blk.tensors
     d, F, R = dims.d, dims.d_ff, dims.B * dims.L
+    for name, got, n, dtype in (("x", x, R * d, torch.bfloat16), ("pos", pos, 3 * R, torch.float32),
+                                ("c", c, dims.B * d, torch.float32)):
+        if got.numel() != n or got.dtype != dtype or not got.is_contiguous():
+            raise ValueError(f"{name}: {got.dtype} {tuple(got.shape)} is not contiguous or does not fit the state's grid")
     shift_a, scale_a, gate_a, shift_m, scale_m, gate_m = (s.mod[:, i * d:(i + 1) * d] for i in range(6))
     a_d, a_f = s.codes[:R * d].view(R, d), s.codes[:R * F].view(R, F)
     y = s.proj.view(-1)[:R * d].view(R, d)
