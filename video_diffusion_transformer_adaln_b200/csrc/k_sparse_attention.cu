@@ -9,7 +9,7 @@
 // products fill the tensor core while the other's softmax runs:
 //   warps 0, 2  TMA for item 0, 1: Q, then the K and V tiles, each into its place
 //               in one ring of slots that all loads share in the order of the MMAs
-//   warp 1      tcgen05.mma from one thread, in the order
+//   warp 1      tcgen05.mma from one elected thread, in the order
 //                 S0(0) S1(0) | PV0(0) S0(1) PV1(0) S1(1) | PV0(1) S0(2) ...
 //               where an item whose list has ended drops out
 //   warp 3      the next pair: takes over a CTA of this grid that has not started
@@ -91,14 +91,38 @@ __device__ __forceinline__ int clamp_len(const int* lens, int b, int L) {
   return lens ? min(max(__ldg(lens + b), 0), L) : L;
 }
 
-// A descriptor whose start address lies `units` of 16 bytes further: the address field is in the low
-// half and does not overflow within shared memory. The volatile add keeps the sums from being kept in
-// registers for every step of every product, which spills.
-__device__ __forceinline__ uint64_t desc_add(uint64_t d, uint32_t units) {
-  uint32_t lo = (uint32_t)d, r;
-  asm volatile("add.u32 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(units));
-  return (d & 0xFFFFFFFF00000000ull) | r;
+// The MMA warp stays converged and one elected thread's predicate `on` is on each of its instructions, so that
+// operands live in uniform registers. Issued from a branch of one thread every MMA takes a dozen moves into those,
+// which queue for issue slots behind the softmax: 168 cycles per MMA against 66 beside two warps per scheduler that
+// issue all the time (128 x 128 x 16 takes 64).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t on;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(on));
+  return on;
 }
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit_to(uint32_t bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(on)
+      : "memory");
+}
+// A value that all lanes hold, known as such to the compiler.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // A copy of its own for each role. A value that lives in all of them is kept on the stack while the softmax
 // needs the registers, and would be reloaded at each of its uses between the MMAs.
@@ -106,6 +130,25 @@ __device__ __forceinline__ uint32_t own_copy(uint32_t v) {
   uint32_t r;
   asm volatile("mov.u32 %0, %1;" : "=r"(r) : "r"(v));
   return r;
+}
+
+// Each lane of four holds four pieces (4 registers each) of a row of its own; afterwards lane i of the four
+// holds piece i of each of the four rows, in the rows' order.
+__device__ __forceinline__ void transpose_quad(uint32_t (&v)[16], int lane) {
+#pragma unroll
+  for (int bit = 1; bit <= 2; bit <<= 1) {
+    const bool up = lane & bit;
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {  // of pieces i (without the bit) and j (with it): keeps one, sends the other
+      const int i = x >> 2, j = i | bit, lo = x, hi = 4 * j + (x & 3);
+      if (i & bit) continue;
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? v[lo] : v[hi], bit);
+      if (up)
+        v[lo] = got;
+      else
+        v[hi] = got;
+    }
+  }
 }
 
 // What an item works on. Kept in shared memory: the softmax threads' registers are the scores'.
@@ -412,95 +455,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (items_done > 0) mbar_wait(bar(Lay::Q_FULL + g), (items_done - 1) & 1, a.err, ERR_WAIT_DRAIN, kDrainLimitNs);
       }
     } else if (warp == 1) {
-      if (lane == 0) {
-        // ---------------- MMA issuer
-        const uint32_t sb = own_copy(sb_), tm = *tmem_slot;
-        auto bar = [&](int place) { return sb + Lay::BAR_OFF + 8u * place; };
-        volatile int* abort_flag = flag_at(sb);
-        bool any = false, ok = true;
-        Place<NS> at;
-        uint32_t tiles_done[2] = {0, 0}, items_done[2] = {0, 0};
-        auto take = [&]() -> bool {
-          return mbar_wait_or_abort(bar(Lay::FULL + at.slot), at.ph, abort_flag, a.err, ERR_WAIT_TMA);
-        };
-        auto give = [&]() {
-          any = true;
-          tc_commit(bar(Lay::EMPTY + at.slot));
-          at.advance(1);
-        };
-        auto issue_s = [&](int g, bool two, bool first, bool last) -> bool {  // S_g = Q_g K^T of the item's next tile
-          if (!take()) return false;
-          tc_fence_after();
-          const uint64_t qd = smem_desc_sw128(sb + Lay::Q_OFF + g * Lay::TILE, 16, 1024);
-          const uint64_t kd = smem_desc_sw128(sb + Lay::RING_OFF + at.slot * Lay::TILE, 16, 1024);
-          if (two) {
+      // ---------------- MMA issuer (whole warp, converged)
+      const uint32_t sb = uniform(sb_), tm = uniform(*tmem_slot), on = elect_one();
+      auto bar = [&](int place) { return sb + Lay::BAR_OFF + 8u * place; };
+      volatile int* abort_flag = flag_at(sb);
+      bool any = false, ok = true;
+      Place<NS> at;
+      uint32_t tiles_done[2] = {0, 0}, items_done[2] = {0, 0};
+      auto wait = [&](int place, uint32_t parity, unsigned code) -> bool {
+        return __all_sync(0xFFFFFFFFu, mbar_wait_or_abort(bar(place), parity, abort_flag, a.err, code));
+      };
+      auto give = [&]() {
+        any = true;
+        commit_to(bar(Lay::EMPTY + at.slot), on);
+        at.advance(1);
+      };
+      auto issue_s = [&](int g, bool two, bool first, bool last) {  // S_g = Q_g K^T of the item's next tile
+        const uint64_t qd = smem_desc_sw128(sb + Lay::Q_OFF + g * Lay::TILE, 16, 1024);
+        const uint64_t kd = smem_desc_sw128(sb + Lay::RING_OFF + at.slot * Lay::TILE, 16, 1024);
+        if (two) {
 #pragma unroll
-            for (int k = 0; k < DH / 16; ++k) {
-              const uint32_t step = ((k >> 2) * kBox + (k & 3) * 32) >> 4;  // of the address field
-              mma_f16(tm + Lay::S_COL(g), desc_add(qd, step), desc_add(kd, step), IDESC_S, k > 0 ? 1u : 0u);
-            }
-          } else {  // one unit: a path of its own, since a choice inside the unrolled one slows every tile
-#pragma unroll 1
-            for (int k = 0; k < DH / 16; ++k) {
-              const uint32_t step = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
-              mma_f16(tm + Lay::S_COL(g), desc_add(qd, step), desc_add(kd, step), IDESC_S_HALF, k > 0 ? 1u : 0u);
-            }
+          for (int k = 0; k < DH / 16; ++k) {
+            const uint32_t step = ((k >> 2) * kBox + (k & 3) * 32) >> 4;  // of the address field
+            mma_ss(tm + Lay::S_COL(g), qd + step, kd + step, IDESC_S, k > 0 ? 1u : 0u, on);
           }
-          if (first) tc_commit(bar(Lay::S_FIRST + g));
-          if (last) tc_commit(bar(Lay::Q_EMPTY + g));
-          give();
-          return true;
-        };
-        auto issue_pv = [&](int g, bool two, bool fresh) -> bool {  // O_g (+)= P_g V
-          if (!mbar_wait_or_abort(bar(Lay::P_FULL + g), tiles_done[g] & 1, abort_flag, a.err, ERR_WAIT_EPI)) return false;
-          ++tiles_done[g];
-          if (!take()) return false;
-          tc_fence_after();
-          const uint64_t vd = smem_desc_sw128(sb + Lay::RING_OFF + at.slot * Lay::TILE, kBox, 1024);
-          if (two) {
-#pragma unroll
-            for (int k = 0; k < kTile / 16; ++k)
-              mma_f16_ts(tm + Lay::O_COL(g), tm + Lay::S_COL(g) + k * 8, desc_add(vd, k * 2048 >> 4), IDESC_PV,
-                         (!fresh || k > 0) ? 1u : 0u);
-          } else {
+        } else {  // one unit: a path of its own, since a choice inside the unrolled one slows every tile
 #pragma unroll 1
-            for (int k = 0; k < kUnit / 16; ++k)
-              mma_f16_ts(tm + Lay::O_COL(g), tm + Lay::S_COL(g) + k * 8, desc_add(vd, k * 2048 >> 4), IDESC_PV,
-                         (!fresh || k > 0) ? 1u : 0u);
+          for (int k = 0; k < DH / 16; ++k) {
+            const uint32_t step = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+            mma_ss(tm + Lay::S_COL(g), qd + step, kd + step, IDESC_S_HALF, k > 0 ? 1u : 0u, on);
           }
-          give();
-          return true;
-        };
-        for (int k = 0; ok; ++k) {
-          const Item* pair = pair_items(sb, k, 1u);
-          if (!pair) { ok = false; break; }
-          const int n0 = pair->tiles, n1 = second(pair)->tiles;
-          if (n0 < 0) break;
-          const int units0 = pair->units, units1 = second(pair)->units;
-          mbar_arrive(bar(Lay::PAIR_EMPTY + k % kPairs));
-          auto first = [&](int g, int units) -> bool {
-            if (units == 0) return true;
-            if (!mbar_wait_or_abort(bar(Lay::Q_FULL + g), items_done[g] & 1, abort_flag, a.err, ERR_WAIT_TMA)) return false;
-            ++items_done[g];
-            return issue_s(g, units > 1, true, units <= 2);
-          };
-          auto round = [&](int g, int units, int n, int t) -> bool {
-            if (t >= n) return true;
-            if (!issue_pv(g, units - 2 * t > 1, t == 0)) return false;
-            if (t + 1 < n) return issue_s(g, units - 2 * (t + 1) > 1, false, t + 2 == n);
-            tc_commit(bar(Lay::FIN + g));
-            return true;
-          };
-          ok = first(0, units0) && first(1, units1);
-          const int n = max(n0, n1);
-          for (int t = 0; t < n && ok; ++t) ok = round(0, units0, n0, t) && round(1, units1, n1, t);
         }
-        if (!ok) {
-          *abort_flag = 1;
-          if (any) {
-            tc_commit(bar(Lay::DRAIN));
-            mbar_wait(bar(Lay::DRAIN), 0, a.err, ERR_WAIT_DRAIN, kDrainLimitNs);
-          }
+        if (first) commit_to(bar(Lay::S_FIRST + g), on);
+        if (last) commit_to(bar(Lay::Q_EMPTY + g), on);
+        give();
+      };
+      auto issue_pv = [&](int g, bool two, bool fresh) {  // O_g (+)= P_g V
+        const uint64_t vd = smem_desc_sw128(sb + Lay::RING_OFF + at.slot * Lay::TILE, kBox, 1024);
+        if (two) {
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_ts(tm + Lay::O_COL(g), tm + Lay::S_COL(g) + k * 8, vd + (k * 2048 >> 4), IDESC_PV,
+                   (!fresh || k > 0) ? 1u : 0u, on);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < kUnit / 16; ++k)
+            mma_ts(tm + Lay::O_COL(g), tm + Lay::S_COL(g) + k * 8, vd + (k * 2048 >> 4), IDESC_PV,
+                   (!fresh || k > 0) ? 1u : 0u, on);
+        }
+        give();
+      };
+      // the slot of the load `by` places on holds its tile
+      auto landed = [&](int by) -> bool {
+        Place<NS> x = at;
+        x.advance(by);
+        return wait(Lay::FULL + x.slot, x.ph, ERR_WAIT_TMA);
+      };
+      for (int k = 0; ok; ++k) {
+        const Item* pair = pair_items(sb, k, 0xFFFFFFFFu);
+        if (!pair) { ok = false; break; }
+        const int n0 = uniform(pair->tiles), n1 = uniform(second(pair)->tiles);
+        if (n0 < 0) break;
+        const int units0 = uniform(pair->units), units1 = uniform(second(pair)->units);
+        if (on) mbar_arrive(bar(Lay::PAIR_EMPTY + k % kPairs));
+        __syncwarp();
+        auto first = [&](int g, int units) -> bool {
+          if (units == 0) return true;
+          if (!wait(Lay::Q_FULL + g, items_done[g] & 1, ERR_WAIT_TMA)) return false;
+          ++items_done[g];
+          if (!landed(0)) return false;
+          tc_fence_after();
+          issue_s(g, units > 1, true, units <= 2);
+          return true;
+        };
+        auto round = [&](int g, int units, int n, int t) -> bool {
+          if (t >= n) return true;
+          // P last: it is what the rounds wait for, and each wait takes some 150 cycles beside the softmax
+          const bool more = t + 1 < n;
+          if (!landed(0) || (more && !landed(1)) || !wait(Lay::P_FULL + g, tiles_done[g] & 1, ERR_WAIT_EPI)) return false;
+          ++tiles_done[g];
+          tc_fence_after();
+          issue_pv(g, units - 2 * t > 1, t == 0);
+          if (more)
+            issue_s(g, units - 2 * (t + 1) > 1, false, t + 2 == n);
+          else
+            commit_to(bar(Lay::FIN + g), on);
+          return true;
+        };
+        ok = first(0, units0) && first(1, units1);
+        const int n = max(n0, n1);
+        for (int t = 0; t < n && ok; ++t) ok = round(0, units0, n0, t) && round(1, units1, n1, t);
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        if (any) {
+          commit_to(bar(Lay::DRAIN), on);
+          mbar_wait(bar(Lay::DRAIN), 0, a.err, ERR_WAIT_DRAIN, kDrainLimitNs);
         }
       }
     } else {
@@ -722,7 +772,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool empty_row = l_run == 0.0f;  // no valid key: O was never written, or only with zeros
         const int b = it->bh / a.n_heads, h = it->bh - b * a.n_heads;
         const int dm = a.n_heads * DH;
-        const long long o_at = ((long long)b * a.Lq + q) * dm + h * DH;
+        // stores go by quads of lanes: 64 bytes of one row at a time (a lane's own row at 16 bytes a time occupies the
+        // load-store unit for 32 cycles an instruction: 4500 to 8700 cycles for the two items)
+        const int first = q - (lane & 3);
+        const long long o_at = ((long long)b * a.Lq + first) * dm + h * DH + (lane & 3) * 8;
         const long long part_at = (long long)item * (DH / 4) * kSparseQueries + row;
         const float inv_l = 1.0f / l_run;
         const float2 il2 = make_float2(inv_l, inv_l);
@@ -750,10 +803,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               pk[e] = empty_row ? 0u : pack_bf16x2(v.x, v.y);
               amax = max3_nan(amax, fabsf(bf16_lo(pk[e])), fabsf(bf16_hi(pk[e])));
             }
-            if (mine && H3B_IDX_OK(o_at + c * 32 + 31, (long long)a.B * a.Lq * dm, a.err)) {
-              uint4* d4 = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + o_at + c * 32);
+            transpose_quad(pk, lane);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) d4[e] = make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) {  // row e of the quad's four, 16 bytes of it per lane
+              const long long at = o_at + (long long)e * dm + c * 32;
+              if (first + e < it->qn && H3B_IDX_OK(at + 7, (long long)a.B * a.Lq * dm, a.err))
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + at) =
+                    make_uint4(pk[4 * e], pk[4 * e + 1], pk[4 * e + 2], pk[4 * e + 3]);
             }
           }
         }
