@@ -55,6 +55,9 @@ constexpr int kSms = 148;               // of a B200
 constexpr int kAhead = 3;              // tiles before a pair's end at which the next is asked for
 constexpr int kItemBytes = 64;
 constexpr float kNoMax = -3.0e38f;     // running maximum before any key
+// Exponents of 2 that a row's maximum may grow before it is raised. Scaled by a power of two, sums lose nothing: they
+// stay finite for |v| up to 2^90. With 8, smooth keys of variance 2 raised it in one tile of five (882 against 798 us).
+constexpr float kGrowth = 16.0f;
 
 struct SparseParams {
   SparseAttnArgs a;
@@ -72,8 +75,8 @@ struct Layout {
   static constexpr int NS = DH == 128 ? 5 : 10;
   static constexpr int Q_OFF = 0, RING_OFF = 2 * TILE;
   static constexpr int BAR_OFF = RING_OFF + NS * TILE;
-  // mbarriers, by their place: per item (two each), per slot, per pair in flight
-  static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FIRST = 4, P_FULL = 6, FIN = 8, FULL = 10, EMPTY = FULL + NS;
+  // mbarriers, by their place: per item (P: per item and half of a tile), per slot, per pair in flight
+  static constexpr int Q_FULL = 0, Q_EMPTY = 2, S_FIRST = 4, P_FULL = 6, FIN = 10, FULL = 12, EMPTY = FULL + NS;
   static constexpr int PAIR_FULL = EMPTY + NS, PAIR_EMPTY = PAIR_FULL + kPairs, CLEAN = PAIR_EMPTY + kPairs;
   static constexpr int ENDING = CLEAN + kPairs, CANCEL = ENDING + 1;
   static constexpr int DRAIN = CANCEL + 1, NBARS = DRAIN + 1;
@@ -295,7 +298,7 @@ __device__ __forceinline__ int taken_cta(uint32_t response) {
   return ok ? (int)x : -1;
 }
 
-template <int DH, int kPolyMod>
+template <int DH>
 __global__ void __launch_bounds__(kThreads, 1)
     sparse_attention_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                             const __grid_constant__ CUtensorMap tmv, const SparseParams p) {
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x < Lay::NBARS) {
     const int i = threadIdx.x;
     // arrivals: P of an item by its softmax warps; a pair is let go by producers, MMA and softmax warps
-    const bool p_full = i >= Lay::P_FULL && i < Lay::P_FULL + 2;
+    const bool p_full = i >= Lay::P_FULL && i < Lay::P_FULL + 4;
     const bool pair_empty = i >= Lay::PAIR_EMPTY && i < Lay::PAIR_EMPTY + kPairs;
     mbar_init(bar(i), p_full ? 4 : pair_empty ? 2 + 1 + 8 : i == Lay::ENDING ? 2 : 1);
     fence_barrier_init();
@@ -490,20 +493,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (last) commit_to(bar(Lay::Q_EMPTY + g), on);
         give();
       };
-      auto issue_pv = [&](int g, bool two, bool fresh) {  // O_g (+)= P_g V
-        const uint64_t vd = smem_desc_sw128(sb + Lay::RING_OFF + at.slot * Lay::TILE, kBox, 1024);
-        if (two) {
+      auto issue_pv = [&](int g, int half, bool fresh) {  // O_g (+)= P_g V, 64 of the tile's keys
+        const uint64_t vd = smem_desc_sw128(sb + Lay::RING_OFF + at.slot * Lay::TILE + half * kUnitBox, kBox, 1024);
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)
-            mma_ts(tm + Lay::O_COL(g), tm + Lay::S_COL(g) + k * 8, vd + (k * 2048 >> 4), IDESC_PV,
-                   (!fresh || k > 0) ? 1u : 0u, on);
-        } else {
-#pragma unroll 1
-          for (int k = 0; k < kUnit / 16; ++k)
-            mma_ts(tm + Lay::O_COL(g), tm + Lay::S_COL(g) + k * 8, vd + (k * 2048 >> 4), IDESC_PV,
-                   (!fresh || k > 0) ? 1u : 0u, on);
-        }
-        give();
+        for (int k = 0; k < kUnit / 16; ++k)
+          mma_ts(tm + Lay::O_COL(g), tm + Lay::S_COL(g) + half * 32 + k * 8, vd + (k * 2048 >> 4), IDESC_PV,
+                 (!fresh || k > 0) ? 1u : 0u, on);
       };
       // the slot of the load `by` places on holds its tile
       auto landed = [&](int by) -> bool {
@@ -532,10 +527,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t >= n) return true;
           // P last: it is what the rounds wait for, and each wait takes some 150 cycles beside the softmax
           const bool more = t + 1 < n;
-          if (!landed(0) || (more && !landed(1)) || !wait(Lay::P_FULL + g, tiles_done[g] & 1, ERR_WAIT_EPI)) return false;
+          const uint32_t parity = tiles_done[g] & 1;
           ++tiles_done[g];
+          if (!landed(0) || (more && !landed(1)) || !wait(Lay::P_FULL + 2 * g, parity, ERR_WAIT_EPI)) return false;
           tc_fence_after();
-          issue_pv(g, units - 2 * t > 1, t == 0);
+          issue_pv(g, 0, t == 0);
+          if (!wait(Lay::P_FULL + 2 * g + 1, parity, ERR_WAIT_EPI)) return false;
+          tc_fence_after();
+          if (units - 2 * t > 1) issue_pv(g, 1, false);
+          give();
           if (more)
             issue_s(g, units - 2 * (t + 1) > 1, false, t + 2 == n);
           else
@@ -642,6 +642,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         return min(kUnit, max(0, it->kn - v * a.block_k - (wide ? (u & 1) * kUnit : 0)));
       };
       float m_run = kNoMax, l_run = 0.0f;
+      // exp2(s * c + nm) of 64 scores, packed to bf16 pairs in their first 32 places; returns the sum
+      auto exponentials = [&](uint32_t* s, float nm) -> float {
+        const float2 nm2 = make_float2(nm, nm);
+        float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int i = 0; i < kUnit; i += 2) {
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, nm2);
+          const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          acc[(i >> 1) & 3] = __fadd2_rn(acc[(i >> 1) & 3], e);
+          s[i >> 1] = pack_bf16x2(e.x, e.y);
+        }
+        const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
+        const float2 a03 = __fadd2_rn(a01, a23);
+        return a03.x + a03.y;
+      };
       const volatile Item* other = g ? pair : second(const_cast<const Item*>(pair));
       Turn<NS> at = place;  // of K_g(t)
       if (g == 1) at.advance(other->tiles > 0);
@@ -679,61 +694,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         at.advance(1);  // to K_g(t + 1)
         if (live) {
-          tc_fence_after();
+          // The exponentials of the first half are taken with the running maximum as it is, while the maximum of
+          // the tile is found. Only where a row's maximum has grown by more than 2^8 (rare after an item's first tile)
+          // is that maximum raised, O rescaled, and the half done again.
           uint32_t sr[kTile];
+          float alpha = 1.0f, part;
+          for (bool again = false;; again = true) {
+            tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < kTile / 32; ++c)
-            tmem_ld32(s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-          tmem_ld_wait();
+            for (int c = 0; c < kTile / 32; ++c)
+              tmem_ld32(s_col + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+            tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < kTile / 32; ++c) tmem_reg_fence(*reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-          if (nv0 < kUnit || nv1 < kUnit) {  // warp-uniform
+            for (int c = 0; c < kTile / 32; ++c) tmem_reg_fence(*reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+            if (nv0 < kUnit || nv1 < kUnit) {  // warp-uniform
 #pragma unroll
-            for (int i = 0; i < kTile; ++i)
-              if ((i & (kUnit - 1)) >= (i < kUnit ? nv0 : nv1)) sr[i] = __float_as_uint(-INFINITY);
-          }
-          // row max with 8 independent partial maxima; NaN if a score is (then the row's sum is NaN too,
-          // whichever pipe computes that score's exponential)
-          float pm[8];
+              for (int i = 0; i < kTile; ++i)
+                if ((i & (kUnit - 1)) >= (i < kUnit ? nv0 : nv1)) sr[i] = __float_as_uint(-INFINITY);
+            }
+            // row max with 8 independent partial maxima; NaN if a score is (then the row's sum is NaN too)
+            float pm[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) pm[e] = __uint_as_float(sr[e]);
+            for (int e = 0; e < 8; ++e) pm[e] = __uint_as_float(sr[e]);
 #pragma unroll
-          for (int i = 8; i < kTile; i += 16)
+            for (int i = 8; i < kTile; i += 16)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) pm[e] = max3_nan(pm[e], __uint_as_float(sr[i + e]), __uint_as_float(sr[i + 8 + e]));
-          const float mx = max3_nan(max3_nan(pm[0], pm[1], pm[2]), max3_nan(pm[3], pm[4], pm[5]), max3_nan(pm[6], pm[7], kNoMax));
-          // finite also where every key of the tile is masked, so that exp2(-inf - m) is 0; an infinite
-          // score makes it NaN, as inf - inf does in the formula
-          const float mxs = fmaf(0.0f, mx, mx * p.scale_log2);
-          float alpha = 1.0f;
-          bool rescale = false;
-          if (t == 0) {
-            m_run = mxs;  // O is not there yet
-          } else if (!(mxs <= m_run + 8.0f)) {  // NaN as well
-            alpha = fast_exp2(m_run - mxs);
-            m_run = mxs;
-            rescale = true;
-          }
-          // p = exp2(s * c - m), packed to bf16 pairs in place; sum with 4 packed accumulators
-          const float2 nm2 = make_float2(-m_run, -m_run);
-          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int i = 0; i < kTile; i += 2) {
-            const float2 x = __ffma2_rn(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), c2, nm2);
-            float2 e;
-            if (kPolyMod > 0 && (i >> 1) % (kPolyMod > 0 ? kPolyMod : 1) == kPolyMod - 1)
-              e = exp2_poly2(x);
-            else
-              e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-            acc[(i >> 1) & 3] = __fadd2_rn(acc[(i >> 1) & 3], e);
-            sr[i >> 1] = pack_bf16x2(e.x, e.y);
-          }
-          const float2 a01 = __fadd2_rn(acc[0], acc[1]), a23 = __fadd2_rn(acc[2], acc[3]);
-          const float2 a03 = __fadd2_rn(a01, a23);
-          l_run = fmaf(l_run, alpha, a03.x + a03.y);
-          // S_g(t) complete => PV_g(t-1) complete: O_g is stable until P_g(t) is published.
-          if (__any_sync(0xFFFFFFFFu, rescale)) {
-#pragma unroll
+              for (int e = 0; e < 8; ++e) pm[e] = max3_nan(pm[e], __uint_as_float(sr[i + e]), __uint_as_float(sr[i + 8 + e]));
+            const float mx = max3_nan(max3_nan(pm[0], pm[1], pm[2]), max3_nan(pm[3], pm[4], pm[5]), max3_nan(pm[6], pm[7], kNoMax));
+            // finite also where every key of the tile is masked, so that exp2(-inf - m) is 0; an infinite
+            // score makes it NaN, as inf - inf does in the formula
+            const float mxs = fmaf(0.0f, mx, mx * p.scale_log2);
+            if (t == 0) m_run = mxs;
+            part = exponentials(sr, -m_run);
+            const bool grown = !(mxs <= m_run + kGrowth);  // NaN as well
+            if (again || t == 0 || !__any_sync(0xFFFFFFFFu, grown)) break;
+            if (grown) {
+              alpha = fast_exp2(m_run - mxs);
+              m_run = mxs;
+            }
+            // S_g(t) complete => PV_g(t-1) complete: O_g is stable until P_g(t) is published.
+#pragma unroll 1
             for (int c = 0; c < DH / 32; ++c) {
               uint32_t o[32];
               tmem_ld32(o_col + c * 32, o);
@@ -749,14 +749,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st32(o_col + c * 32, o);
             }
           }
-          // P_g(t) over the first 64 columns of S_g: column c holds keys 2c (low half) and 2c+1.
+          // P_g(t) over the first 64 columns of S_g: column c holds keys 2c (low half) and 2c+1. Its first half is
+          // multiplied while the second is formed.
           tmem_st32(s_col, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-          tmem_st32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(Lay::P_FULL + 2 * g));
+          part += exponentials(sr + kUnit, -m_run);
+          tmem_st32(s_col + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[kUnit]));
+          l_run = fmaf(l_run, alpha, part);
           tmem_st_wait();
         }
         tc_fence_before();  // P is there, and O of the item before has been read
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(Lay::P_FULL + g));
+        if (lane == 0) {
+          if (!live) mbar_arrive(bar(Lay::P_FULL + 2 * g));
+          mbar_arrive(bar(Lay::P_FULL + 2 * g + 1));
+        }
       }
       if (!ok) break;
       if (it->tiles > 0) {
@@ -780,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float inv_l = 1.0f / l_run;
         const float2 il2 = make_float2(inv_l, inv_l);
         float amax = 0.0f;
-#pragma unroll
+#pragma unroll 1  // unrolled, most of its time is the fetch of instructions that run once an item
         for (int c = 0; c < DH / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(o_col + c * 32, o);
@@ -950,7 +960,7 @@ cudaError_t launch(const SparseAttnArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   tmv = tmk;  // of the same shape: encoding a third map costs the host a microsecond
   if (!set_tmap_address(&tmv, a.v)) return cudaErrorInvalidValue;
-  auto k = sparse_attention_kernel<DH, 4>;
+  auto k = sparse_attention_kernel<DH>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Lay::SMEM);
   if (e != cudaSuccess) return e;
   e = launch_pdl(k, dim3((unsigned)((items + p.per_cta - 1) / p.per_cta)), dim3(kThreads), Lay::SMEM, st, tmq, tmk, tmv, p);
