@@ -923,24 +923,27 @@ __global__ void __launch_bounds__(256) sparse_join_kernel(const SparseParams p) 
 }
 
 // Items per list. In units of a tile of a CTA with one item (1.77 us): a tile of two items at once takes 1.2, an
-// item's start and end 1.3 in each round of CTAs; joining 2.5, and for each part 0.02 with 128 query rows. The rule
-// takes the split with the least time. 148 SMs, whatever the device has: the workspace's size must not depend on
-// the device. Measured with 100 queries over 36 tiles: 8 lists in one part each 73 us, as the rule splits them
-// 16 us; 40 lists 75 and 28 us, 160 lists 91 and 83 us.
+// item's start and end 1.3 in each round of CTAs; no less than 0.0065 for each tile of all lists, their keys and
+// values from HBM at head_dim 128; joining 2.7, and for each part 0.023 with 128 query rows. The rule takes the split
+// with the least time. 148 SMs, whatever the device has: the workspace's size must not depend on the device. Measured
+// with 100 queries over 36 tiles: 8 lists in one part each 64 us, as the rule splits them (18 parts) 15.4 us; 40 lists
+// 66 and (6) 29.8 us, 80 lists 67 and (3) 49.5 us; 160 lists, which it leaves whole, 81 us, in three parts 92 us.
 struct Split {
   int n, tiles;  // items per list, tiles per item
 };
-Split choose_split(long long rows, int Lq, int topk, int block_k) {
+Split choose_split(long long rows, int Lq, int head_dim, int topk, int block_k) {
   const int tiles = (topk * (block_k / kUnit) + 1) / 2;
+  const double memory = 0.0065 * head_dim / 128 * (double)rows * tiles;
   Split best{1, tiles};
   double best_cost = -1.0;
   for (int n = 1; n <= kMaxSplit && n <= tiles; ++n) {
     const int per = (tiles + n - 1) / n, used = (tiles + per - 1) / per;
     const long long items = rows * used;
     const double rounds = items <= kSms ? (double)per : (double)(((items + 1) / 2 + kSms - 1) / kSms) * (1.2 * per + 1.3);
-    const double joined = used > 1 ? 2.5 + 0.02 * (double)items * std::min(Lq, kSparseQueries) / kSparseQueries : 0.0;
-    if (best_cost < 0 || rounds + joined < best_cost) {
-      best_cost = rounds + joined;
+    const double joined = used > 1 ? 2.7 + 0.023 * (double)items * std::min(Lq, kSparseQueries) / kSparseQueries : 0.0;
+    const double cost = std::max(rounds, memory) + joined;
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
       best = {used, per};
     }
   }
@@ -953,7 +956,7 @@ cudaError_t launch(const SparseAttnArgs& a, cudaStream_t st) {
   SparseParams p{};
   p.a = a;
   p.rows = a.B * a.n_heads * a.nqb;
-  const Split sp = choose_split(p.rows, a.Lq, a.topk, a.block_k);
+  const Split sp = choose_split(p.rows, a.Lq, DH, a.topk, a.block_k);
   p.nsplit = sp.n;
   p.split_tiles = sp.tiles;
   p.scale_log2 = 1.4426950408889634f / sqrtf((float)DH);
@@ -982,7 +985,7 @@ cudaError_t launch(const SparseAttnArgs& a, cudaStream_t st) {
 size_t sparse_attn_ws_bytes(int B, int n_heads, int head_dim, int Lq, int nqb, int topk, int block_k) {
   const long long rows = (long long)B * n_heads * nqb;
   if (Lq == 1) return sparse_rows_ws_bytes(rows, head_dim, topk, block_k);
-  const Split sp = choose_split(rows, Lq, topk, block_k);
+  const Split sp = choose_split(rows, Lq, head_dim, topk, block_k);
   return sp.n > 1 ? (size_t)rows * sp.n * kSparseQueries * (head_dim * 4 + 8) : 0;
 }
 
