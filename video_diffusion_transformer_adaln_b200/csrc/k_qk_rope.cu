@@ -16,6 +16,11 @@
 //   warp 9      stores finished boxes and frees their slots
 // The boxes, ordered by tokens, then by heads, are dealt out evenly to as many
 // CTAs as are resident.
+//
+// 18432 tokens, 40 heads of 128: 200 us, 5.66 TB/s, 0.86 of a copy. Rows loaded to and
+// stored from registers, with the next ones on their way: 218 us. A box stored by one
+// tensor copy instead of a bulk copy per head: 198 us, for three more tensor maps that
+// cost the host as much as a small call takes.
 #include <algorithm>
 
 #include "h3b_common.cuh"

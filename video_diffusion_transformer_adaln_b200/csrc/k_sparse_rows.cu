@@ -16,6 +16,10 @@
 //               their own running maximum and sum. At the end of a row all of these are
 //               joined and written to the workspace.
 // A second kernel joins the parts of a row that several CTAs have worked on.
+//
+// 4 streams, 40 heads of 128 over 8 key heads, 72 of 288 blocks of 64: 51 us for 377 MB of
+// gathered rows, 7.4 TB/s of HBM and L2 (the whole cache once from HBM: 46 us). Rows loaded
+// straight to registers 106 us; consumers in two groups of four warps 55 us.
 #include <algorithm>
 
 #include "h3b_common.cuh"
