@@ -116,9 +116,12 @@ __global__ void __launch_bounds__(kMeanThreads) block_means_kernel(const SelectA
   }
 }
 
-// The order of the scores as unsigned integers: higher is better, -0 equals +0, NaN is last.
+// The order of the scores as unsigned integers: higher is better, -0 equals +0, NaN is last. Minus infinity has
+// 0x000FFFFF in its upper half. No key's upper half is zero, so the histograms' ranges, which start at a key's upper
+// half, start above zero: the threshold of a range taken from its start on can be lowered by one.
+constexpr unsigned long long kKeyNan = 1ull << 32;
 __device__ __forceinline__ unsigned long long order_key(double s) {
-  if (s != s) return 1ull;
+  if (s != s) return kKeyNan;
   const unsigned long long u = (unsigned long long)__double_as_longlong(s + 0.0);
   return (u >> 63) ? ~u : u | 0x8000000000000000ull;
 }
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const SelectA
           range = 1ull << min(sh, 8);
           sh = max(0, sh - 8);
         }
-        if (ties == n) T -= 1;  // keys >= T, as keys above T - 1 (T > 0: no key is zero)
+        if (ties == n) T -= 1;  // keys >= T, as keys above T - 1 (T >= lo > 0)
       }
       int at = 0, seen = 0;  // listed, and equal to T, so far
       for (int j0 = 0; j0 < n && at < want; j0 += 32) {
