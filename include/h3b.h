@@ -483,8 +483,7 @@ H3B_API h3b_status h3b_sparse_workspace_size(const h3b_sparse_dims* dims, size_t
 
 /* The key blocks each query block attends. The score of a pair is the product of
  * the mean of the query block's valid rows and the mean of the key block's valid
- * rows, summed in 64 bits (the rows of a mean in pairs in 32 bits first, which is
- * exact for values within a factor of 2^15 of each other). Of the key blocks that hold a valid key, the topk (or
+ * rows, summed in 64 bits. Of the key blocks that hold a valid key, the topk (or
  * all, if fewer) with the highest scores are listed in ascending order in
  * `blocks`, and their number is written to `counts`; unused entries are -1. Ties
  * go to the lower block; a NaN score ranks last. A query block without a valid

@@ -10,7 +10,7 @@
 // from L2; the topk of a row is found by a warp, by histograms over the scores
 // mapped to unsigned integers.
 //
-// 18432 tokens, 40 heads of 128, 36 of 288 blocks: 100 us; the means 65 (5.8 TB/s, 0.89
+// 18432 tokens, 40 heads of 128, 36 of 288 blocks: 105 us; the means 69 (5.8 TB/s, 0.89
 // of a copy), the scores 18 (the means of all keys of a head, 295 KB, from L2 for each
 // CTA), the lists 17 (a warp's chain through a row). Scores on the FP64 vector pipe, topk
 // by bisection: 143 us; threads per CTA of 128 to 512 and two or three CTAs per SM: 100
@@ -43,8 +43,9 @@ Means means_of(void* ws, int B, int n_heads, int n_kv_heads, int DH, int nqb, in
 }
 
 // A warp per block of rows: DH / 8 lanes per row, so 32 / (DH / 8) rows at a time, kBatch of them in
-// flight while the batch before is added. Rows are added in pairs in 32 bits (two bf16 values of like size
-// add exactly) and the pairs in 64, which halves the conversions and additions on the FP64 pipe.
+// flight while the batch before is added. Every value is converted before it is added: pairs added in 32 bits first
+// would halve the conversions (100 us in place of 105 at the size above), but lose what is 2^16 below its partner, and
+// with it the order of near scores and the ties of blocks that hold the same rows in another order.
 constexpr int kBatch = 8;  // loads per lane and batch
 
 template <int DH>
@@ -64,13 +65,12 @@ __device__ __forceinline__ void block_mean(const __nv_bfloat16* p, int n, int la
   };
   auto add = [&](const uint4(&v)[kBatch]) {
 #pragma unroll
-    for (int i = 0; i < kBatch; i += 2) {
+    for (int i = 0; i < kBatch; ++i) {
       const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-      const uint32_t y[4] = {v[i + 1].x, v[i + 1].y, v[i + 1].z, v[i + 1].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        s[2 * e] += (double)(bf16_lo(x[e]) + bf16_lo(y[e]));
-        s[2 * e + 1] += (double)(bf16_hi(x[e]) + bf16_hi(y[e]));
+        s[2 * e] += (double)bf16_lo(x[e]);
+        s[2 * e + 1] += (double)bf16_hi(x[e]);
       }
     }
   };
