@@ -152,6 +152,22 @@ class SparseBlockState:
         nqb = self.sparse.nqb
         self.blocks, self.counts = e(B, H, nqb, topk, dtype=torch.int32), e(B, H, nqb, dtype=torch.int32)
         self.ws = e(h3b.h3b_sparse_workspace_size(self.sparse), dtype=torch.uint8)
+        self.device = self.ws.device  # with its index
+        f32 = torch.float32
+        # what each tensor of a call has to be: type, and shape or number of elements
+        self.inputs = {"x": (torch.bfloat16, R * d), "pos": (f32, 3 * R), "c": (f32, B * d)}
+        self.norms = {"q": (f32, dh), "k": (f32, dh), "post_attn": (f32, d), "post_mlp": (f32, d)}
+        self.weights = {"w_ada": (torch.bfloat16, (6 * d, d)), "b_ada": (f32, 6 * d)}
+        for w, sw, b, n, k in (("wqkv", "sqkv", "bqkv", 3 * d, d), ("wo", "so", "bo", d, d), ("w1", "s1", "b1", F, d),
+                               ("w2", "s2", "b2", d, F)):
+            self.weights.update({w: (torch.int8, (n, k)), sw: (f32, n), b: (f32, n)})
+
+    def check(self, name: str, got: torch.Tensor, dtype, size):
+        """Refuses a tensor that the kernels, which get its address alone, would read as something else."""
+        fits = got.shape == size if isinstance(size, tuple) else got.numel() == size
+        if not fits or got.dtype != dtype or not got.is_contiguous() or got.device != self.device or got.data_ptr() % 16:
+            raise ValueError(f"{name}: {got.dtype} {tuple(got.shape)} on {got.device} is not contiguous from a 16-byte boundary, "
+                             f"or does not fit the state's grid and device ({dtype}, {size}, {self.device})")
 
 
 def sparse_block_forward(state: SparseBlockState, blk: DeviceBlock, norms: Dict[str, torch.Tensor], c: torch.Tensor,
@@ -163,14 +179,26 @@ def sparse_block_forward(state: SparseBlockState, blk: DeviceBlock, norms: Dict[
       O = softmax over the listed key blocks;          x += gate_attn * (RMS(quant(O) Wo^T) * post_attn)
       A3 = quant(LN(x)(1 + scale_mlp) + shift_mlp);    x += gate_mlp * (RMS(quant(GELU(A3 W1^T)) W2^T) * post_mlp)
 
-    norms: fp32 vectors "q", "k" [head_dim] and "post_attn", "post_mlp" [d] (missing ones: see h3b_qk_norm_rope and
-    h3b_residual_norm). The listed blocks stay in state.blocks and state.counts."""
+    norms: fp32 vectors "q", "k" [head_dim] and "post_attn", "post_mlp" [d] (missing ones, or None: see h3b_qk_norm_rope
+    and h3b_residual_norm). The listed blocks stay in state.blocks and state.counts. ValueError, before any launch, for
+    tensors and weights that do not fit the state's grid, for unknown norms, and where the current device is not the
+    state's."""
     s, dims, t = state, state.dims, blk.tensors
     d, F, R = dims.d, dims.d_ff, dims.B * dims.L
-    for name, got, n, dtype in (("x", x, R * d, torch.bfloat16), ("pos", pos, 3 * R, torch.float32),
-                                ("c", c, dims.B * d, torch.float32)):
-        if got.numel() != n or got.dtype != dtype or not got.is_contiguous():
-            raise ValueError(f"{name}: {got.dtype} {tuple(got.shape)} is not contiguous or does not fit the state's grid")
+    if s.device.type == "cuda" and s.device.index != torch.cuda.current_device():
+        raise ValueError(f"the state's device is {s.device}, the current one cuda:{torch.cuda.current_device()}")
+    for name, got in (("x", x), ("pos", pos), ("c", c)):
+        s.check(name, got, *s.inputs[name])
+    for name, got in norms.items():
+        if name not in s.norms:
+            raise ValueError(f"norms: {name!r} is none of {list(s.norms)}")
+        if got is not None:
+            s.check(f"norms[{name!r}]", got, *s.norms[name])
+    for name, want in s.weights.items():
+        if t.get(name) is not None:
+            s.check(name, t[name], *want)
+        elif name[0] != "b":
+            raise ValueError(f"{name} is missing")
     shift_a, scale_a, gate_a, shift_m, scale_m, gate_m = (s.mod[:, i * d:(i + 1) * d] for i in range(6))
     a_d, a_f = s.codes[:R * d].view(R, d), s.codes[:R * F].view(R, F)
     y = s.proj.view(-1)[:R * d].view(R, d)
