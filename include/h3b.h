@@ -332,6 +332,9 @@ H3B_API int h3b_profile_read(h3b_kernel_time* out, int max_entries);
  * Step entry points. Each runs one step of the block on caller buffers; the
  * block entry points above chain exactly these kernels. They exist so every
  * step can be checked on its own.
+ * Every absmax (given, computed here or max-combined) is NaN where a value of its
+ * row is, and infinite where one is; the row's scale s is then NaN or infinite, so
+ * that its products do not pass for finite ones, and its codes have no meaning.
  * ------------------------------------------------------------------------- */
 
 /* AdaLN Linear ([README] "Int8 양자화", gated AdaLN; [MLX] "性能上限"):
@@ -512,9 +515,8 @@ H3B_API h3b_status h3b_attention_blocks(const h3b_sparse_dims* dims, const void*
  * branch's norm, in one pass over rows of d channels:
  *   x_out = bf16(x + alpha * gate * (post_norm(y) * w_post))
  *   h     = bf16(pre_norm(x_out) * (1 + scale) + shift)
- *   h_out = h, and q, s = the per-row int8 quantizer of h (as h3b_quantize_rows)
- * a row with a NaN or an infinity gets a NaN or infinite s, so that its products
- *   do not pass for finite ones, and codes without a meaning.
+ *   h_out = h, and q, s = the per-row int8 quantizer of h (as h3b_quantize_rows,
+ *   rows with a NaN or an infinity included)
  * y, x, x_out, h_out bf16 [rows][d]; q int8 [rows][d]; s fp32 [rows].
  * post_norm, pre_norm: 0 none, 1 RMS (x * rsqrt(mean(x^2) + eps)), 2 LayerNorm
  * (no affine, biased variance). x_out may be x; otherwise no output may overlap

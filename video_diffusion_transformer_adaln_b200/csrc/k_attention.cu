@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(attn::kThreads, 1)
         for (int e = 0; e < 16; ++e) {
           const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), il2);
           pk[e] = pack_bf16x2(v.x, v.y);
-          amax = max3f(amax, fabsf(bf16_lo(pk[e])), fabsf(bf16_hi(pk[e])));
+          amax = max3_nan(amax, fabsf(bf16_lo(pk[e])), fabsf(bf16_hi(pk[e])));
         }
         if (q < L && H3B_IDX_OK(((long long)b * L + q) * dm + h * DH + c * 32 + 31, (long long)a.B * L * dm, a.err)) {
           uint4* d4 = reinterpret_cast<uint4*>(dst + c * 32);

@@ -312,7 +312,7 @@ __device__ __forceinline__ void epilogue_tile(const GemmArgs& p, uint32_t tbase,
             const float2 gv = gelu_tanh2(make_float2(v[e], v[e + 1]));
             v[e] = round_bf16(gv.x);
             v[e + 1] = round_bf16(gv.y);
-            amax = fmaxf(amax, fmaxf(fabsf(v[e]), fabsf(v[e + 1])));
+            amax = max3_nan(amax, fabsf(v[e]), fabsf(v[e + 1]));
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);

@@ -141,11 +141,6 @@ __global__ void __launch_bounds__(256) adaln_gemv_kernel(const __nv_bfloat16* __
 // rounded fp32 absmax is the absmax of the rounded h.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float2 bf16x2_to_f2(uint32_t u) { return make_float2(bf16_lo(u), bf16_hi(u)); }
-__device__ __forceinline__ float max3f_row(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 
 constexpr int kLnMaxWarps = 32;
 
@@ -290,7 +285,7 @@ __global__ void __launch_bounds__(1024, 1) ln_mod_quant_kernel(
         const float2 y = __fmul2_rn(f[4 * i + e], rstd2);
         const float2 h = __ffma2_rn(y, make_float2(m.x, m.y), make_float2(m.z, m.w));
         u[e] = pack_bf16x2(h.x, h.y);
-        am = max3f_row(am, fabsf(h.x), fabsf(h.y));
+        am = max3_nan(am, fabsf(h.x), fabsf(h.y));
       }
       v[i] = make_uint4(u[0], u[1], u[2], u[3]);
     }
@@ -298,7 +293,7 @@ __global__ void __launch_bounds__(1024, 1) ln_mod_quant_kernel(
     if (lane == 0) rd[2 * kLnMaxWarps + warp] = amax;
     group_sync();
     amax = 0.0f;
-    for (int k = 0; k < wpr; ++k) amax = fmaxf(amax, rd[2 * kLnMaxWarps + w0 + k]);
+    for (int k = 0; k < wpr; ++k) amax = max_nan(amax, rd[2 * kLnMaxWarps + w0 + k]);
     amax = round_bf16(amax);  // = the max of the rounded |h|
     if (valid) {
       if (h_out) {
@@ -450,13 +445,13 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ i
       float f[8];
       load8<T>(r + v * 8, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+      for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(f[e]));
     }
     m = warp_max(m);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
     __syncthreads();
     m = red[0];
-    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) m = fmaxf(m, red[w]);
+    for (int w = 1; w < (int)(blockDim.x >> 5); ++w) m = max_nan(m, red[w]);
     amax = m;
   }
   const float sc = __fdiv_rn(amax, 127.0f);
