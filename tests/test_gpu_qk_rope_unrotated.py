@@ -1,5 +1,5 @@
 """Lanes that no axis rotates pass as they are: beside an infinity, and minus zeros with their sign. Without weights
-they are a copy, bit for bit, whatever the head holds."""
+they are a copy, bit for bit, whatever else the head holds (a NaN stays a NaN)."""
 import pytest
 import torch
 
