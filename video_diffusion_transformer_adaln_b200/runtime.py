@@ -161,13 +161,19 @@ class SparseBlockState:
         for w, sw, b, n, k in (("wqkv", "sqkv", "bqkv", 3 * d, d), ("wo", "so", "bo", d, d), ("w1", "s1", "b1", F, d),
                                ("w2", "s2", "b2", d, F)):
             self.weights.update({w: (torch.int8, (n, k)), sw: (f32, n), b: (f32, n)})
+        self.needed = [name for name in self.weights if not name.startswith("b")]  # biases may be missing
 
-    def check(self, name: str, got: torch.Tensor, dtype, size):
-        """Refuses a tensor that the kernels, which get its address alone, would read as something else."""
-        fits = got.shape == size if isinstance(size, tuple) else got.numel() == size
-        if not fits or got.dtype != dtype or not got.is_contiguous() or got.device != self.device or got.data_ptr() % 16:
-            raise ValueError(f"{name}: {got.dtype} {tuple(got.shape)} on {got.device} is not contiguous from a 16-byte boundary, "
-                             f"or does not fit the state's grid and device ({dtype}, {size}, {self.device})")
+    def check(self, tensors: Dict[str, Optional[torch.Tensor]], wanted: Dict[str, tuple], what: str = ""):
+        """Refuses tensors that the kernels, which get their addresses alone, would read as something else."""
+        device = self.device
+        for name, got in tensors.items():
+            if got is None:
+                continue
+            dtype, size = wanted[name]
+            if ((got.numel() if type(size) is int else got.shape) != size or got.dtype is not dtype or not got.is_contiguous()
+                    or got.device != device or got.data_ptr() & 15):
+                raise ValueError(f"{what}{name}: {got.dtype} {tuple(got.shape)} on {got.device} is not contiguous from a "
+                                 f"16-byte boundary, or does not fit the state's grid and device ({dtype}, {size}, {device})")
 
 
 def sparse_block_forward(state: SparseBlockState, blk: DeviceBlock, norms: Dict[str, torch.Tensor], c: torch.Tensor,
@@ -187,18 +193,16 @@ def sparse_block_forward(state: SparseBlockState, blk: DeviceBlock, norms: Dict[
     d, F, R = dims.d, dims.d_ff, dims.B * dims.L
     if s.device.type == "cuda" and s.device.index != torch.cuda.current_device():
         raise ValueError(f"the state's device is {s.device}, the current one cuda:{torch.cuda.current_device()}")
-    for name, got in (("x", x), ("pos", pos), ("c", c)):
-        s.check(name, got, *s.inputs[name])
-    for name, got in norms.items():
-        if name not in s.norms:
-            raise ValueError(f"norms: {name!r} is none of {list(s.norms)}")
-        if got is not None:
-            s.check(f"norms[{name!r}]", got, *s.norms[name])
-    for name, want in s.weights.items():
-        if t.get(name) is not None:
-            s.check(name, t[name], *want)
-        elif name[0] != "b":
+    s.check({"x": x, "pos": pos, "c": c}, s.inputs)
+    unknown = norms.keys() - s.norms.keys()
+    if unknown:
+        raise ValueError(f"norms: {sorted(unknown)}, known are {list(s.norms)}")
+    s.check(norms, s.norms, "norms: ")
+    weights = {name: t.get(name) for name in s.weights}
+    for name in s.needed:
+        if weights[name] is None:
             raise ValueError(f"{name} is missing")
+    s.check(weights, s.weights)
     shift_a, scale_a, gate_a, shift_m, scale_m, gate_m = (s.mod[:, i * d:(i + 1) * d] for i in range(6))
     a_d, a_f = s.codes[:R * d].view(R, d), s.codes[:R * F].view(R, F)
     y = s.proj.view(-1)[:R * d].view(R, d)
