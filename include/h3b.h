@@ -443,8 +443,10 @@ H3B_API h3b_status h3b_gemm_i8_gelu(const int8_t* A, const float* sA, const int8
  *        with h, the next rope_w with w, each part even, their sum at most
  *        head_dim; the lanes after them pass unrotated. Pair (2j, 2j+1) of a
  *        part of length r turns by pos * rope_theta^(-2j/r); the angle is formed
- *        and reduced in 64 bits, so positions far from zero lose nothing.
- *   Norm and rotation are in fp32, each output rounded once; V is copied.
+ *        and reduced in 64 bits and is off by less than 2^-46 of itself, below
+ *        the rotation's own 32 bits for angles up to 2^23 radians.
+ *   Norm and rotation are in fp32 (squares too: |x| below 2^60), each output
+ *   rounded once; V is copied.
  *   n_heads >= 1, n_kv_heads >= 1, n_heads + n_kv_heads <= 1024, head_dim in
  *   {64, 128}, B*L < 2^31; B*L == 0 is an empty problem. */
 typedef struct {
@@ -492,7 +494,9 @@ H3B_API h3b_status h3b_sparse_workspace_size(const h3b_sparse_dims* dims, size_t
  * go to the lower block; a NaN score ranks last. A query block without a valid
  * row gets no key block. Always listed, ahead of any score: blocks
  * [0, keep_first), and with keep_local > 0 the blocks that hold the positions of
- * the query block itself and keep_local - 1 more on each side. */
+ * the query block itself and keep_local - 1 more on each side. Query i stands at
+ * position i of the keys, whatever Lq and Lk are: for queries that stand
+ * elsewhere (new tokens late in a long latent) leave keep_local at 0. */
 H3B_API h3b_status h3b_select_blocks(const h3b_sparse_dims* dims, const void* q, const void* k, const int* q_lens,
                                      const int* kv_lens, int* blocks, int* counts, void* ws, size_t ws_bytes,
                                      h3b_stream stream);
@@ -503,9 +507,12 @@ H3B_API h3b_status h3b_select_blocks(const h3b_sparse_dims* dims, const void* q,
  *   absmax fp32 [B*Lq] or NULL: each row's max |o| is max-combined into it
  *   (zero it first; rows behind q_lens are left as they were); a NaN among them
  *   makes it NaN.
- * A query whose list holds no valid key gets o = 0. counts NULL: every list has
- * topk entries; a count is clamped to [0, topk]. An entry outside [0, nkb) holds
- * no key; a block listed twice counts its keys twice. */
+ * A query whose list holds no valid key gets o = 0, as does one whose valid keys
+ * all score minus infinity; a NaN or plus infinity among its scores makes o NaN.
+ * counts NULL: every list has topk entries; a count is clamped to [0, topk]. An
+ * entry outside [0, nkb) holds no key; a block listed twice counts its keys
+ * twice. The sums are in 32 bits, ahead of their division: finite for values of
+ * v up to 2^90. */
 H3B_API h3b_status h3b_attention_blocks(const h3b_sparse_dims* dims, const void* q, const void* k, const void* v,
                                         const int* q_lens, const int* kv_lens, const int* blocks,
                                         const int* counts, void* o, float* absmax, void* ws, size_t ws_bytes,
@@ -519,7 +526,7 @@ H3B_API h3b_status h3b_attention_blocks(const h3b_sparse_dims* dims, const void*
  *   rows with a NaN or an infinity included)
  * y, x, x_out, h_out bf16 [rows][d]; q int8 [rows][d]; s fp32 [rows].
  * post_norm, pre_norm: 0 none, 1 RMS (x * rsqrt(mean(x^2) + eps)), 2 LayerNorm
- * (no affine, biased variance). x_out may be x; otherwise no output may overlap
+ * (no affine, biased variance), in fp32 (squares too: |x| below 2^57). x_out may be x; otherwise no output may overlap
  * an input or another output.
  *   w_post fp32 [d] or NULL (ones). gate, shift, scale: fp32 [d] per item of
  *   rows_per_item rows, mod_stride floats (a multiple of 4) apart; NULL is gate

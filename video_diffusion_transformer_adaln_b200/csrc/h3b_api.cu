@@ -948,7 +948,7 @@ h3b_status h3b_qk_norm_rope(const h3b_qk_dims* dims, const void* qkv, const floa
   a.B = d.B; a.L = d.L; a.n_heads = d.n_heads; a.n_kv_heads = d.n_kv_heads; a.head_dim = d.head_dim;
   a.row_stride = d.row_stride; a.eps = d.norm_eps; a.err = di->err;
   a.qkv = qkv; a.wq = wq; a.wk = wk; a.pos = pos; a.q = q; a.k = k; a.v = v;
-  // theta^(-2j/r) / pi by repeated multiplication: within 64 * 2^-53 of the power
+  // theta^(-2j/r) / pi by repeated multiplication: within 128 * 2^-53 of the power (64 roundings, and the first power's)
   const int part[3] = {d.rope_t, d.rope_h, d.rope_w};
   int p = 0;
   for (int ax = 0; ax < 3; ++ax) {
