@@ -1,6 +1,6 @@
-// Device helpers shared by the attention kernels (k_attention.cu,
-// k_sparse_attention.cu): exponentials, the three-way maximum and the MMA whose
-// A operand lies in tensor memory.
+// Device helpers of the attention kernels: the exponential that all of them use,
+// and what the dense one (k_attention.cu) has besides: exponentials on the FMA
+// pipe, a three-way maximum and the MMA whose A operand lies in tensor memory.
 #pragma once
 
 #include "h3b_common.cuh"

@@ -10,11 +10,11 @@
 // from L2; the topk of a row is found by a warp, by histograms over the scores
 // mapped to unsigned integers.
 //
-// 18432 tokens, 40 heads of 128, 36 of 288 blocks: 105 us; the means 69 (5.8 TB/s, 0.89
-// of a copy), the scores 18 (the means of all keys of a head, 295 KB, from L2 for each
-// CTA), the lists 17 (a warp's chain through a row). Scores on the FP64 vector pipe, topk
-// by bisection: 143 us; threads per CTA of 128 to 512 and two or three CTAs per SM: 100
-// to 112 us.
+// 18432 tokens, 40 heads of 128, 36 of 288 blocks: 105 us; the means 70 (5.6 TB/s, 0.85
+// of a copy; conversions take 66% of their pipe), the scores 18 (the means of all keys of a
+// head, 295 KB, from L2 for each CTA), the lists 17 (a warp's chain through a row). With means
+// of 65 us, that added pairs in 32 bits: scores on the FP64 vector pipe, topk by bisection 143
+// us; threads per CTA of 128 to 512 and two or three CTAs per SM 100 to 112 us, these 100.
 #include "h3b_common.cuh"
 #include "h3b_internal.h"
 

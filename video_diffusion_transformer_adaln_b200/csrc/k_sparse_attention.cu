@@ -29,11 +29,12 @@
 //
 // Bound by the chain of an item's tile: from S to the softmax 350 cycles, the first half of
 // the exponentials 800 to 1100, from P to the MMA warp 300, P V and the next S 770. The two
-// items of a pair cover that to about 3300 cycles for a tile of each, of which the tensor
-// core works 2048. 18432 tokens, 40 heads of 128, 36 of 288 blocks of 64 keys: 800 us,
-// 1085 TFLOP/s; 900 us where the power limit holds the clock at 1.6 GHz. The exponentials
-// all go to the MUFU pipe (a fourth of them as polynomials: 864 us). Tiles of 64 keys with
-// S computed one tile ahead: 900 us.
+// items of a pair cover that to about 3800 cycles for a tile of each (the slope over lists of
+// 12 to 144 blocks, at 1.96 GHz), of which the tensor core works 2048; a pair's start and end
+// add about 9000. 18432 tokens, 40 heads of 128, 36 of 288 blocks of 64 keys: 784 us,
+// 1109 TFLOP/s; back to back, where the power limit lowers the clock, 868 to 936 us. The
+// exponentials all go to the MUFU pipe (a fourth of them as polynomials 8% slower). Tiles of
+// 64 keys with S computed one tile ahead: 12% slower.
 //
 // Units without a valid key (entries outside the key blocks, blocks behind
 // kv_len) are loaded from behind the tensor, where TMA fills zeros. In the one
@@ -705,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         at.advance(1);  // to K_g(t + 1)
         if (live) {
           // The exponentials of the first half are taken with the running maximum as it is, while the maximum of
-          // the tile is found. Only where a row's maximum has grown by more than 2^8 (rare after an item's first tile)
+          // the tile is found. Only where a row's maximum has grown by more than 2^16 (rare after an item's first tile)
           // is that maximum raised, O rescaled, and the half done again.
           uint32_t sr[kTile];
           float alpha = 1.0f, part;
